@@ -13,8 +13,9 @@ global scale per head and side) in pages of `page` tokens. Three operators work 
 Head counts follow the linear layers of the 27B-class model that the library's GEMM workloads use: 6144 = (40 + 2 * 4)
 * 128 columns of QKV and 5120 = 40 * 128 of the output projection, over 64 layers. The other sizes are generic.
 
-A page of one layer: for each KV head, page * D/2 bytes of key codes (element 2j in the low nibble of byte j),
-page * D/16 key scales, then the same two for the values.
+A page of one layer holds, for each KV head: key codes [page][D/2] (element 2j in the low nibble of byte j), key scales
+[page][D/16], value codes in groups of four tokens and eight elements [page/4][D/8][4 tokens][4 bytes], and value scales
+[D/16][page].
 """
 import math
 import random
@@ -207,11 +208,19 @@ def _parents(c):
 # ----------------------------------------------------------------------------------------------------- the inputs
 
 def _heads(pages, c):
-    """Views of a pool [pages][bytes]: key codes, key scales, value codes, value scales [pages][heads][page][...]."""
+    """Views of a pool [pages][bytes]: key codes and scales [pages][heads][page][...], value codes
+    [pages][heads][page/4][4][D/8][4], value scales [pages][heads][page][D/16]."""
     p, d, h = c["page"], c["head_dim"], c["kv_heads"]
     x = pages[:, :_page_bytes(c)].unflatten(1, (h, p * d * 9 // 8))
     cuts = [0, p * d // 2, p * d * 9 // 16, p * d * 17 // 16, p * d * 9 // 8]
-    return [x[:, :, a:b].unflatten(2, (p, (b - a) // p)) for a, b in zip(cuts, cuts[1:])]
+    k, ks, v, vs = (x[:, :, a:b] for a, b in zip(cuts, cuts[1:]))
+    return [k.unflatten(2, (p, d // 2)), ks.unflatten(2, (p, d // 16)),
+            v.unflatten(2, (p // 4, d // 8, 4, 4)).transpose(3, 4), vs.unflatten(2, (d // 16, p)).transpose(2, 3)]
+
+
+def _tokens(v_codes, page, at):
+    """The value codes [T][heads][D/2] of tokens by page and place."""
+    return v_codes[page, :, at // 4, at % 4].flatten(2)
 
 
 def _quantize(x, g):
@@ -339,8 +348,11 @@ def _prepare_attention(c, gen):
             if side == 0:
                 x *= 1.0 + 5.0 * ((torch.arange(hkv * d, device="cuda").reshape(hkv, 1, d) * 7919) % 97 < 4).float()
             codes, scales = _quantize(x, g.reshape(hkv, 1, 1))
-            for at, new in ((side, codes), (side + 1, scales)):
-                sections[at][lo:hi] = torch.where(keep, new, sections[at][lo:hi])
+            kept = keep
+            if side == 2:                                       # four tokens to a group
+                codes, kept = codes.unflatten(2, (p // 4, 4)).unflatten(4, (d // 8, 4)), keep.unflatten(2, (p // 4, 4))[..., None]
+            sections[side][lo:hi] = torch.where(kept, codes, sections[side][lo:hi])
+            sections[side + 1][lo:hi] = torch.where(keep, scales, sections[side + 1][lo:hi])
     t, most = sum(counts), max(counts)
     q = (torch.randn((t, c["q_heads"], d), generator=gen, device="cuda") * 0.7).to(DTYPES[c["dtype"]])
     start = torch.tensor([0] + counts, device="cuda").cumsum(0).int()
@@ -455,10 +467,11 @@ def _plain_append(s):
     page, at = s["slots"][fits] // p, s["slots"][fits] % p
     g_k, g_v = s["k_g"].reshape(hkv, 1), s["v_g"].reshape(hkv, 1)
     k_codes[page, :, at], k_scales[page, :, at] = _quantize(_rotate(s["k"], s)[fits], g_k)
-    v_codes[page, :, at], v_scales[page, :, at] = _quantize(s["v"][fits].float(), g_v)
+    codes, v_scales[page, :, at] = _quantize(s["v"][fits].float(), g_v)
+    v_codes[page, :, at // 4, at % 4] = codes.unflatten(2, (-1, 4))
     page, at = s["slots"].clamp(min=0) // p, s["slots"].clamp(min=0) % p
     k = _values(k_codes[page, :, at], k_scales[page, :, at]) / g_k
-    v = _values(v_codes[page, :, at], v_scales[page, :, at]) / g_v
+    v = _values(_tokens(v_codes, page, at), v_scales[page, :, at]) / g_v
     keep = fits[:, None, None]
     return {"q": s["q_out"], "k": torch.where(keep, k, 0.0).to(s["k"].dtype), "v": torch.where(keep, v, 0.0).to(s["k"].dtype)}
 
@@ -467,7 +480,9 @@ def _plain_attention(s):
     c = s["case"]
     p, d, hq, hkv, b, most = c["page"], c["head_dim"], c["q_heads"], c["kv_heads"], c["batch"], s["most"]
     width = max(1, -(-c["max_len"] // p))
-    held = [x[s["table"][:, :width].long().clamp(min=0)].permute(0, 2, 1, 3, 4).flatten(2, 3) for x in _heads(s["pages"], c)]
+    held = [x[s["table"][:, :width].long().clamp(min=0)].transpose(1, 2) for x in _heads(s["pages"], c)]
+    held[2] = held[2].flatten(5).flatten(3, 4)                             # value codes token by token again
+    held = [x.flatten(4).flatten(2, 3) for x in held]
     g_k, g_v = s["k_g"].reshape(hkv, 1, 1), s["v_g"].reshape(hkv, 1, 1)
     k = _values(held[0], held[1]) / g_k                                    # [batch][kv head][key][D]
     v = _values(held[2], held[3]) / g_v
@@ -648,10 +663,11 @@ def _exact_attention(c, s):
             see[:, n - new:] = s["mask"][rows, count - new:count]
         for h in range(hkv):
             x = raw[:, h]
-            cut = [x[:, a:e].reshape(-1, (e - a) // p)[:n] for a, e in
-                   ((0, p * d // 2), (p * d // 2, p * d * 9 // 16), (p * d * 9 // 16, p * d * 17 // 16), (p * d * 17 // 16, size))]
-            k = number(cut[0], cut[1]) / s["k_g"][h].double()
-            v = number(cut[2], cut[3]) / s["v_g"][h].double()
+            codes, scales = x[:, :p * d // 2].reshape(-1, d // 2), x[:, p * d // 2:p * d * 9 // 16].reshape(-1, d // 16)
+            k = number(codes[:n], scales[:n]) / s["k_g"][h].double()
+            codes = x[:, p * d * 9 // 16:p * d * 17 // 16].reshape(-1, d // 8, 4, 4).permute(0, 2, 1, 3).reshape(-1, d // 2)
+            scales = x[:, p * d * 17 // 16:].reshape(-1, d // 16, p).permute(0, 2, 1).reshape(-1, d // 16)
+            v = number(codes[:n], scales[:n]) / s["v_g"][h].double()
             for j in range(h * group, (h + 1) * group):
                 z = (s["q"][rows, j].double() @ k.T) * s["scale"]
                 z = torch.where(see, z, -math.inf)
