@@ -397,7 +397,7 @@ def _prepare_pages(c, gen):
         b = torch.arange(c["batch"], device="cuda")
         step = torch.randint(1, 2 * c["page"], (c["batch"],), generator=gen, device="cuda")
         room = (table.shape[1] * c["page"])
-        new = torch.where(b % 4 == 0, 0, torch.where(b % 4 == 1, (n - step).clamp(min=0), (n + step).clamp(max=room)))
+        new = torch.where(b % 4 == 3, 0, torch.where(b % 4 == 1, (n - step).clamp(min=0), (n + step).clamp(max=room)))
         s["new_lens"] = new.int()
         return s
     size = c["layers"] * c["pool"] * _page_bytes(c)
