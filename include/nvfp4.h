@@ -8,6 +8,9 @@
  *   W4A4:  D[m][n] = alpha * sum_k (A[m][k] * SFA[m][k/16]) * (B[n][k] * SFB[n][k/16])
  *   W4A16: y[m][n] = alpha * sum_k  x[m][k] * (W[n][k] * SFW[n][k/16])
  *
+ * and, for the attention between two such layers, a key/value cache in the same
+ * format (nvfp4_kv_*: append with rotary positions, read, attention, pages).
+ *
  * A, B, W hold 4-bit E2M1 codes packed two per byte along K (element 2j in the
  * low nibble of byte j); SFA, SFB, SFW hold one E4M3 (or UE4M3) scale byte per
  * 16 consecutive K-elements of a row; x and y are BF16; alpha is FP32 and is
@@ -323,6 +326,178 @@ nvfp4_status nvfp4_quantize_two_pass_tiled(const uint16_t *x, int64_t rows, int6
  * does it up front. Arguments, outputs and errors as for nvfp4_quantize_tiled. */
 nvfp4_status nvfp4_quantize_tiled_noalloc(const uint16_t *x, int64_t rows, int64_t K, uint8_t *a_tiled,
                                           float *g_dev, float *inv_g_dev, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Key/value cache in NVFP4.
+ *
+ * Keys and values are held as E2M1 codes with one E4M3 scale byte per 16
+ * consecutive values of a head and one FP32 global scale per head and side, in
+ * pages of page_size tokens of one layer. A held value stands for
+ * code * scale / g. One page holds, for each KV head h at byte
+ * h * page_size * head_dim * 9/8, with P = page_size and D = head_dim:
+ *   key codes     [P][D/2]            element 2j in the low nibble of byte j
+ *   key scales    [P][D/16]
+ *   value codes   [P/4][D/8][4][4]    (token group, element octet, token, byte)
+ *   value scales  [D/16][P]
+ * (values grouped so that a lane of the attention kernel finds the eight
+ * elements of four tokens in 16 consecutive bytes, and their scales in 4).
+ * A token's slot is page * P + place in the page. */
+typedef enum { NVFP4_F32 = 0, NVFP4_BF16 = 1, NVFP4_F16 = 2 } nvfp4_dtype;
+
+typedef struct {
+  uint8_t *pages;        /* device, 16-byte aligned */
+  int64_t num_pages;     /* 0 .. 2^31 - 1 */
+  int64_t page_stride;   /* bytes from page to page: >= nvfp4_kv_page_bytes, % 16 == 0 */
+  int32_t page_size;     /* tokens of a page: 16, 32, 64, 128 or 256 */
+  int32_t kv_heads;      /* 1 .. 65535 */
+  int32_t head_dim;      /* 16 .. 256, % 16 == 0 */
+  int32_t reserved;      /* 0 */
+  const float *k_g;      /* device FP32 [kv_heads], global scales of the keys (finite, > 0), or NULL: 1 */
+  const float *v_g;      /* the same of the values */
+} nvfp4_kv_cache;
+
+/* Rotary positions. Pair j of a head (j < rot_dim / 2; elements j and j +
+ * rot_dim/2, or 2j and 2j+1 when interleaved) turns by the angle that cos and
+ * sin hold in row positions[axis_of[j]][token], column j:
+ *   a' = a cos - b sin,  b' = b cos + a sin   (FP32, each operation rounded).
+ * Elements from rot_dim on stay as they are. A position outside the table gives
+ * NaN. */
+typedef struct {
+  const float *cos, *sin;       /* device FP32 [max_pos][rot_dim / 2] */
+  const int32_t *positions;     /* device [axes][tokens], axis rows position_stride apart */
+  const uint8_t *axis_of;       /* device [rot_dim / 2]: the axis of each pair (< axes), or NULL: axis 0 */
+  int64_t max_pos;
+  int64_t position_stride;
+  int32_t rot_dim;              /* even, 0 .. head_dim (0: no rotation; the pointers may be NULL) */
+  int32_t axes;                 /* 1 .. 255 */
+  int32_t interleaved;          /* 0 or 1 */
+  int32_t reserved;             /* 0 */
+} nvfp4_rope;
+
+/* A [tokens][heads][head_dim] tensor: element strides of tokens and heads, the
+ * last dimension contiguous. base 16-byte aligned, both strides % 8 == 0. */
+typedef struct {
+  void *base;
+  int64_t token_stride, head_stride;
+} nvfp4_rows;
+
+/* Bytes of one page (kv_heads * page_size * head_dim * 9/8); 0 when page_size,
+ * kv_heads or head_dim is not one that the cache takes. */
+size_t nvfp4_kv_page_bytes(int32_t page_size, int32_t kv_heads, int32_t head_dim);
+
+/* Turns queries and keys to their positions and quantizes keys and values into
+ * their slots.
+ *  k, v   [tokens][kv_heads][head_dim] of `dtype` (NVFP4_BF16 or NVFP4_F16).
+ *  q      base NULL: no queries; else [tokens][q_heads][head_dim] of `dtype`,
+ *         written turned (rounded once to dtype) to q_out, which may be q.
+ *  slots  device int64 [tokens]; a slot outside the pool (-1 for the padding
+ *         rows of a captured graph) writes nothing. Slots of one call are
+ *         distinct.
+ *  rope   NULL: no rotation (q is copied).
+ * The turned key stays in FP32 until it is quantized, by nvfp4_quantize's steps
+ * under its head's global scale; there is no tensor maximum to wait for, so a
+ * block past 2688 / g saturates. A block with a NaN gets scale byte 0x7F and
+ * reads as NaN; an infinity saturates. tokens == 0 is a no-op. */
+nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache *cache, nvfp4_rows k, nvfp4_rows v, nvfp4_rows q, nvfp4_rows q_out,
+                             int dtype, int64_t tokens, int32_t q_heads, const int64_t *slots,
+                             const nvfp4_rope *rope, void *stream);
+
+/* Reads slots back: k and v [tokens][kv_heads][head_dim] of `dtype` (any of the
+ * three) get fl32(code * scale / g), rounded once more for the 16-bit types.
+ * A slot outside the pool reads as zeros. */
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int64_t *slots, int64_t tokens, int dtype, nvfp4_rows k,
+                           nvfp4_rows v, void *stream);
+
+/* Attention of a ragged batch over its pages: for query i of sequence b's
+ * n = q_start[b+1] - q_start[b], at position p = lens[b] - n + i,
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,   lse = ln sum_j exp(scale * q . k_j)
+ * over the keys j < lens[b] that it may see: all of them; with causal, j <= p;
+ * with window > 0 (which needs causal), j > p - window too; with a mask, the
+ * keys before the n new ones, and new key t (j = lens[b] - n + t) when
+ * mask[row][t] != 0 (a mask replaces causal and excludes window). A query that
+ * sees no key gets out = 0 and lse = -inf. What lies in masked or unused slots
+ * (NaN scales too) does not reach the result. Query head h reads KV head
+ * h / (q_heads / kv_heads).
+ *  q       [total_q][q_heads][head_dim] of dtype BF16 or F16; out the same.
+ *  table   device int32 [batch][>= max_pages], rows table_stride apart: page ids
+ *          in order of position. Only the ceil(lens[b] / page_size) first are
+ *          read; an id outside the pool masks its keys.
+ *  lens    device int32 [batch]: tokens in the cache, the new ones included
+ *          (taken as 0 .. max_pages * page_size).
+ *  q_start device int32 [batch + 1], ascending, or NULL: one query per sequence
+ *          (total_q == batch).
+ *  max_q   at least the longest sequence's n; queries of a sequence past it are
+ *          not computed. The kernels are chosen by it.
+ *  mask    device uint8 [total_q][max_q], rows mask_stride apart, or NULL.
+ *  lse     device FP32 [total_q][q_heads], or NULL.
+ *  ws      nvfp4_kv_attention_workspace_bytes(...) bytes, 16-byte aligned, no
+ *          initialisation needed; one per stream that runs concurrently.
+ * Long sequences are split over the CUs and joined in a fixed order: results
+ * are bit-identical from call to call. */
+typedef struct {
+  float scale;              /* finite, > 0 */
+  int32_t causal;           /* 0 or 1 */
+  int64_t window;           /* 0: none */
+  const uint8_t *mask;
+  int64_t mask_stride;
+} nvfp4_kv_mask;
+size_t nvfp4_kv_attention_workspace_bytes(const nvfp4_kv_cache *cache, int64_t total_q, int32_t q_heads, int64_t batch,
+                                          int64_t max_pages, int64_t max_q);
+nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache *cache, nvfp4_rows q, int dtype, int64_t total_q, int32_t q_heads,
+                                const int32_t *table, int64_t table_stride, int64_t max_pages, const int32_t *lens,
+                                const int32_t *q_start, int64_t batch, int64_t max_q, const nvfp4_kv_mask *mask,
+                                nvfp4_rows out, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* Page management. A page is free when its reference count (int32, one per page
+ * of the pool) is <= 0; pages are taken lowest id first. The bookkeeping runs
+ * on the device with no host synchronisation. Pools: `layers` layers,
+ * layer_stride bytes apart, each num_pages pages of page_bytes bytes,
+ * page_stride apart (all % 16 == 0, base 16-byte aligned). Outputs may be the
+ * inputs (in place). Tables are int32 [batch][width], rows *_stride apart, -1
+ * where there is no page.
+ *  ws   nvfp4_kv_pages_workspace_bytes(num_pages, batch) bytes (batch: that of
+ *       the table, or the children of a fork), 16-byte aligned, not initialised. */
+typedef struct {
+  uint8_t *base;
+  int64_t layers, layer_stride, num_pages, page_stride, page_bytes;
+} nvfp4_kv_pool;
+size_t nvfp4_kv_pages_workspace_bytes(int64_t num_pages, int64_t batch);
+
+/* Copies page src[i] to page dst[i], i < n, in every layer (device int32 ids;
+ * pairs with an id outside the pool are skipped). No page may be both source
+ * and destination, nor a destination twice. */
+nvfp4_status nvfp4_kv_copy_pages(const nvfp4_kv_pool *pool, const int32_t *src, const int32_t *dst, int64_t n,
+                                 void *stream);
+
+/* Forks sequences: child c shares the whole pages of sequence parents[c] (their
+ * counts go up by one) and gets a copy of its partly filled page, if there is
+ * one, in a page taken from the pool. Children are served in order; one that
+ * finds no page, or has no such parent, or whose parent's length or partly
+ * filled page is out of range, gets a row of -1 and is counted in short_dev
+ * (device int32).
+ *  child_table [children][width]; refs_out [num_pages]; refs_out may be refs. */
+nvfp4_status nvfp4_kv_fork(const nvfp4_kv_pool *pool, int32_t page_size, const int32_t *table, int64_t table_stride,
+                           int64_t width, int64_t batch, const int32_t *lens, const int32_t *refs,
+                           const int32_t *parents, int64_t children, int32_t *child_table, int64_t child_stride,
+                           int32_t *refs_out, int32_t *short_dev, void *ws, size_t ws_bytes, void *stream);
+
+/* Gives back and takes pages as sequences go from lens[b] to new_lens[b] tokens
+ * (0: the sequence ends): first the entries past ceil(new / page_size) lose a
+ * reference and become -1, then new entries take free pages in the order of
+ * sequences and positions. Entries that find no page stay -1 and are counted in
+ * short_dev. Lengths are taken as 0 .. width * page_size. A shared page that
+ * becomes partly filled stays shared: fork before appending to it. */
+nvfp4_status nvfp4_kv_resize(int64_t num_pages, int32_t page_size, const int32_t *table, int64_t table_stride,
+                             int64_t width, int64_t batch, const int32_t *lens, const int32_t *new_lens,
+                             const int32_t *refs, int32_t *table_out, int64_t table_out_stride, int32_t *refs_out,
+                             int32_t *short_dev, void *ws, size_t ws_bytes, void *stream);
+
+/* Packs a pool: with n live pages (reference count > 0), the live pages with id
+ * >= n move, in order, to the free ids below n, in order; the table's entries
+ * and the counts follow, and live_dev (device int32) gets n. */
+nvfp4_status nvfp4_kv_compact(const nvfp4_kv_pool *pool, const int32_t *table, int64_t table_stride, int64_t width,
+                              int64_t batch, const int32_t *refs, int32_t *table_out, int64_t table_out_stride,
+                              int32_t *refs_out, int32_t *live_dev, void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -11,6 +11,9 @@ Entry points (same names as the C ABI):
                   ws=None, alpha_col=None)
   nvfp4_gemm_w4a16(x, w_prep, N, K, alpha=1.0, alpha_dev=None, out=None, ws=None, alpha_col=None)
   nvfp4_quantize(x, codes=None, scales=None, g=None, inv_g=None, ws=None)
+and, on a key/value cache held in NVFP4 (kv_cache.py):
+  nvfp4_kv_append, nvfp4_kv_read, nvfp4_kv_attention, nvfp4_kv_copy_pages, nvfp4_kv_fork, nvfp4_kv_resize,
+  nvfp4_kv_compact
 """
 import ctypes
 import os
@@ -43,9 +46,42 @@ class Config(ctypes.Structure):
 
 _CFG = ctypes.POINTER(Config)
 
+
+class _Cache(ctypes.Structure):
+    """nvfp4_kv_cache"""
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("k_g", ctypes.c_void_p), ("v_g", ctypes.c_void_p)]
+
+
+class _Rope(ctypes.Structure):
+    """nvfp4_rope"""
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("axis_of", ctypes.c_void_p), ("max_pos", ctypes.c_int64), ("position_stride", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int32), ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class _Rows(ctypes.Structure):
+    """nvfp4_rows"""
+    _fields_ = [("base", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Mask(ctypes.Structure):
+    """nvfp4_kv_mask"""
+    _fields_ = [("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("window", ctypes.c_int64),
+                ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64)]
+
+
+class _Pool(ctypes.Structure):
+    """nvfp4_kv_pool"""
+    _fields_ = [("base", ctypes.c_void_p), ("layers", ctypes.c_int64), ("layer_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("page_bytes", ctypes.c_int64)]
+
 # C signatures: (name, restype, argtypes)
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_I32 = ctypes.c_int32
 _SIGS = [
     ("nvfp4_init", ctypes.c_int, [ctypes.c_int]),
     ("nvfp4_status_str", ctypes.c_char_p, [ctypes.c_int]),
@@ -69,6 +105,21 @@ _SIGS = [
     ("nvfp4_gemm_w4a4_two_pass_tiled", ctypes.c_int,
      [_P, _P, _I64, _I64, _I64, ctypes.c_float, _P, _P, _P, ctypes.c_int, _I64, _CFG, _P, ctypes.c_size_t, _P]),
     ("nvfp4_quantize_tiled_noalloc", ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P]),
+    ("nvfp4_kv_page_bytes", ctypes.c_size_t, [_I32, _I32, _I32]),
+    ("nvfp4_kv_append", ctypes.c_int,
+     [_P, _Rows, _Rows, _Rows, _Rows, ctypes.c_int, _I64, _I32, _P, _P, _P]),
+    ("nvfp4_kv_read", ctypes.c_int, [_P, _P, _I64, ctypes.c_int, _Rows, _Rows, _P]),
+    ("nvfp4_kv_attention_workspace_bytes", ctypes.c_size_t, [_P, _I64, _I32, _I64, _I64, _I64]),
+    ("nvfp4_kv_attention", ctypes.c_int,
+     [_P, _Rows, ctypes.c_int, _I64, _I32, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _Rows, _P, _P, ctypes.c_size_t, _P]),
+    ("nvfp4_kv_pages_workspace_bytes", ctypes.c_size_t, [_I64, _I64]),
+    ("nvfp4_kv_copy_pages", ctypes.c_int, [_P, _P, _P, _I64, _P]),
+    ("nvfp4_kv_fork", ctypes.c_int,
+     [_P, _I32, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("nvfp4_kv_resize", ctypes.c_int,
+     [_I64, _I32, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("nvfp4_kv_compact", ctypes.c_int,
+     [_P, _P, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
 ]
 EXPORTED = [s[0] for s in _SIGS]
 
@@ -520,3 +571,8 @@ def nvfp4_gemm_w4a4_two_pass_tiled(a2_tiled, M, w_prep, N, K, alpha=1.0, alpha_d
                                                 _ptr(alpha_dev), _ptr(alpha_col), _ptr(out), code, _ld(out, M, N),
                                                 _cfg_arg(config), wsp, nws, _stream()))
     return out
+
+
+from .kv_cache import (KVCache, nvfp4_kv_append, nvfp4_kv_attention, nvfp4_kv_attention_workspace,  # noqa: E402,F401
+                       nvfp4_kv_compact, nvfp4_kv_copy_pages, nvfp4_kv_fork, nvfp4_kv_page_bytes, nvfp4_kv_read,
+                       nvfp4_kv_resize)

@@ -1,0 +1,825 @@
+// Attention over the NVFP4 key/value cache.
+//
+// For a query row q and the keys it sees,  t_j = scale * q . k_j,
+//   out = sum_j e^(t_j - m) v_j / sum_j e^(t_j - m),   lse = m + ln sum_j e^(t_j - m),
+// in one pass over the keys with a running reference m: when a tile's largest
+// t passes m by more than a factor 2^8, the sums so far are scaled down to the
+// new m. Any m gives the same quotient, so m need not be the exact maximum.
+//
+// The rows of one KV head are its queries times the query heads of its group:
+// row r is query r / G, head r % G of the group. Both products run on the
+// matrix cores transposed, S^T = K Q^T and O^T = V^T P^T, in 16 x 16 x 32 FP16
+// steps: a column of S^T and of O^T is one query row and stays in the same
+// lanes, so the softmax's scaling of O needs no exchange between lanes, and
+// P^T leaves the exponential already in the layout that the second product
+// takes (the order of its 32 keys is free as long as V's matches).
+//
+// Precision. code * scale has 6 significant bits and lies in [2^-10, 2688], so
+// it is exact in FP16. Each query row is scaled by a power of two to a largest
+// magnitude in [2^8, 2^9), which keeps every bit of a BF16 or FP16 element down
+// to 2^-22 of the row's largest. P is rounded to FP16 (11 bits, where BF16
+// would keep 8) after a factor 2^6, which puts its range at 2^14 .. 2^-24 under
+// the lazy reference; the row sums use the unrounded FP32 values. All
+// accumulators, maxima and sums are FP32; global scales enter in FP32 at the
+// end (k_g into the softmax's factor, v_g into the last division).
+#include <math.h>
+
+#include "kv_common.hpp"
+
+namespace nvfp4 {
+
+static constexpr int kWaves = 4;
+static constexpr int kTile = 32;                       // keys of one wave's step
+static constexpr int kStep = kWaves * kTile;           // keys of one workgroup's step
+static constexpr int kTargetWgs = 1024;                // workgroups that a call is split into when it has fewer
+static constexpr float kHeadroom = 8.0f;               // log2 of how far a value may pass the reference
+static constexpr float kOffset = 6.0f;                 // log2 of the factor on P
+
+struct AttnArgs {
+  KvView kv;
+  const uint16_t *q;
+  uint16_t *out;
+  float *lse;
+  int64_t q_t, q_h, o_t, o_h;
+  int64_t total_q, table_stride;
+  const int32_t *table, *lens, *q_start;
+  const uint8_t *mask;
+  int64_t mask_stride;
+  float scale;
+  int32_t batch, max_pages, max_q, window;
+  int32_t group;             // query heads of a KV head
+  int32_t causal;
+  int32_t target;            // workgroups per KV head to split into
+  int32_t slots;             // pieces that the workspace holds for each KV head
+  float *part_o;             // workspace: partial sums [slot][row][D], then [slot][row][2] of (m, l)
+  float *part_ml;
+};
+
+// ------------------------------------------------------------------- plan
+
+// One sequence's share of the work; keys in steps of kStep, rows in tiles of RT.
+struct Seq {
+  int len, queries, first;   // keys, queries computed, row of the first one
+  int row_tiles, steps;      // steps: the most that one row tile has
+};
+
+template <int RT>
+__device__ __forceinline__ Seq sequence(const AttnArgs &A, int b) {
+  Seq s;
+  const int64_t most = (int64_t)A.max_pages << A.kv.log_p;
+  const int n = A.lens[b];
+  s.len = n < 0 ? 0 : (int64_t)n > most ? (int)most : n;
+  int64_t q0 = b, q1 = b + 1;
+  if (A.q_start) {
+    q0 = min(max((int64_t)A.q_start[b], (int64_t)0), A.total_q);
+    q1 = min(max((int64_t)A.q_start[b + 1], q0), A.total_q);
+  }
+  s.first = (int)q0;
+  s.queries = (int)(q1 - q0);                 // of which the first max_q are computed
+  const int used = min(s.queries, A.max_q);
+  s.row_tiles = (used * A.group + RT - 1) / RT;
+  int span = s.len;
+  if (A.window) span = (int)min((int64_t)span, (int64_t)A.window + (RT + A.group - 2) / A.group + kTile);
+  s.steps = (span + kStep - 1) / kStep;
+  return s;
+}
+
+__device__ __forceinline__ int wave_sum_scan(int v) {   // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(v, off, 64);
+    if (lane >= off) v += y;
+  }
+  return v;
+}
+
+// A workgroup's unit: one row tile of one sequence, and one of the `splits` pieces of its keys.
+struct Unit {
+  int b, tile, split, splits, slot;
+};
+
+__device__ __forceinline__ int splits_of(const Seq &s, int chunk) { return max(1, (s.steps + chunk - 1) / chunk); }
+
+// Steps a piece may have: the whole call's steps over the workgroups to fill.
+template <int RT>
+__device__ __forceinline__ int chunk_steps(const AttnArgs &A) {
+  int total = 0;
+  for (int base = 0; base < A.batch; base += 64) {
+    const int b = base + (threadIdx.x & 63);
+    int w = 0;
+    if (b < A.batch) {
+      const Seq s = sequence<RT>(A, b);
+      w = s.row_tiles * s.steps;
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) w += __shfl_xor(w, off, 64);
+    total += w;
+  }
+  return max(1, (total + A.target - 1) / A.target);
+}
+
+// Finds unit `u` (COMBINE: split row tile `u`); false past the last. Every wave does it for itself.
+template <int RT, bool COMBINE>
+__device__ __forceinline__ bool find_unit(const AttnArgs &A, int u, Unit *out) {
+  const int chunk = chunk_steps<RT>(A);
+  int units = 0, slots = 0;
+  for (int base = 0; base < A.batch; base += 64) {
+    const int b = base + (threadIdx.x & 63);
+    int mine = 0, part = 0, splits = 1;
+    if (b < A.batch) {
+      const Seq s = sequence<RT>(A, b);
+      splits = splits_of(s, chunk);
+      mine = COMBINE ? (splits > 1 ? s.row_tiles : 0) : s.row_tiles * splits;
+      part = splits > 1 ? s.row_tiles * splits : 0;
+    }
+    const int to = units + wave_sum_scan(mine), slot_to = slots + wave_sum_scan(part);
+    const uint64_t hit = __ballot(u < to);
+    if (hit) {
+      const int lane = __builtin_ctzll(hit);
+      const int first = __builtin_amdgcn_readlane(to - mine, lane);
+      const int slot = __builtin_amdgcn_readlane(slot_to - part, lane);
+      const int n = __builtin_amdgcn_readlane(splits, lane);
+      out->b = base + lane;
+      out->splits = n;
+      if (COMBINE) {
+        out->tile = u - first;
+        out->split = 0;
+      } else {
+        out->tile = (u - first) / n;
+        out->split = (u - first) - out->tile * n;
+      }
+      out->slot = slot + out->tile * n + out->split;
+      return true;
+    }
+    units = __builtin_amdgcn_readlane(to, 63);
+    slots = __builtin_amdgcn_readlane(slot_to, 63);
+  }
+  return false;
+}
+
+// The keys that query i of a sequence sees: [lo, hi) (under a tree mask, those before the new ones).
+struct Range {
+  int lo, hi;
+};
+
+__device__ __forceinline__ Range keys_of(const AttnArgs &A, const Seq &s, int i) {
+  Range r;
+  r.lo = 0;
+  r.hi = s.len;
+  if (A.mask) {
+    r.hi = max(0, s.len - s.queries);
+  } else if (A.causal) {
+    const int pos = s.len - s.queries + i;
+    r.hi = max(0, min(s.len, pos + 1));
+    if (A.window) r.lo = min(r.hi, max(0, pos + 1 - A.window));
+  }
+  return r;
+}
+
+// ------------------------------------------------------------------ tiles
+
+// 32 keys of one wave as they lie in the cache. Lane (g = lane / 16, m = lane % 16) holds, for
+// each half of 16 keys, key m's codes of elements [g * DP / 4, (g + 1) * DP / 4) with their
+// scales, and the codes of values m * VD .. m * VD + VD - 1 of keys 4 g .. 4 g + 3 with theirs.
+template <int DP>
+struct Tile {
+  static constexpr int KS = DP / 32;                   // products of 32 along a key's elements
+  static constexpr int NB = DP / 64;                   // scale blocks of a lane's key elements
+  static constexpr int VD = DP / 16;                   // value elements of a lane
+  static constexpr int NU = DP == 256 ? 2 : 1;         // octets of value elements that a lane loads
+  uint32_t kw[2][KS];
+  uint32_t ks[2];
+  u32x4_t vw[2][NU];
+  uint32_t vs[2];
+};
+
+// What does not change from tile to tile: byte offsets of a lane in a head's part of a page.
+struct LaneOffsets {
+  uint32_t k, ks, v, vs;
+};
+
+template <int DP>
+__device__ __forceinline__ LaneOffsets lane_offsets(const KvView &kv) {
+  const uint32_t lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+  const uint32_t D = kv.D, octets = D / 8, blocks = D / 16;
+  LaneOffsets o;
+  // Lanes past the head's elements read some in-page bytes that are multiplied by zero: a key
+  // row may be overrun by up to 56 bytes, which the sections behind it always hold.
+  o.k = m * (D / 2) + g * (DP / 8);
+  o.ks = kv.k_scales() + m * blocks + min(g * (DP / 64), blocks - 1);
+  const uint32_t octet = DP == 64 ? m / 2 : DP == 128 ? m : 2 * m;
+  o.v = kv.v_codes() + g * (D * 2) + min(octet, octets - (DP == 256 ? 2 : 1)) * 16;
+  o.vs = kv.v_scales() + (min(octet / 2, blocks - 1) << kv.log_p) + 4 * g;
+  return o;
+}
+
+template <int N>
+__device__ __forceinline__ uint32_t load_bytes(const uint8_t *p) {
+  uint32_t r = 0;
+  if (N == 1) {
+    r = *p;
+  } else {
+    if (N == 2) {
+      uint16_t h;
+      __builtin_memcpy(&h, p, 2);
+      r = h;
+    } else {
+      __builtin_memcpy(&r, p, 4);
+    }
+  }
+  return r;
+}
+
+template <int DP>
+__device__ __forceinline__ void load_half(const KvView &kv, const LaneOffsets &o, const uint8_t *head, uint32_t at,
+                                          Tile<DP> &t, int st) {
+  const uint8_t *codes = head + at * (uint32_t)(kv.D / 2);
+#pragma unroll
+  for (int i = 0; i < Tile<DP>::KS / 4; i++) {
+    const u32x4_t w = *reinterpret_cast<const u32x4_a4 *>(codes + o.k + 16 * i);
+#pragma unroll
+    for (int j = 0; j < 4; j++) t.kw[st][4 * i + j] = w[j];
+  }
+  if (Tile<DP>::KS == 2) {
+    const u32x2_t w = *reinterpret_cast<const u32x2_a4 *>(codes + o.k);
+    t.kw[st][0] = w[0], t.kw[st][1] = w[1];
+  }
+  t.ks[st] = load_bytes<Tile<DP>::NB>(head + at * (uint32_t)(kv.D / 16) + o.ks);
+#pragma unroll
+  for (int u = 0; u < Tile<DP>::NU; u++) t.vw[st][u] = *reinterpret_cast<const u32x4_t *>(codes + o.v + 16 * u);
+  t.vs[st] = *reinterpret_cast<const uint32_t *>(head + at + o.vs);
+}
+
+// Loads the 32 keys from `base` on; bit st of the result: half st lies in a page of the pool.
+template <int DP>
+__device__ __forceinline__ uint32_t load_tile(const KvView &kv, const LaneOffsets &o, const int32_t *row, int cols,
+                                              int64_t head_at, int base, Tile<DP> &t) {
+  uint32_t ok = 0;
+#pragma unroll
+  for (int st = 0; st < 2; st++) {
+    const int key = base + 16 * st;
+    const int col = key >> kv.log_p;
+    const int page = col < cols ? row[col] : -1;
+    const bool in = page >= 0 && page < kv.num_pages;
+    if (in) ok |= 1u << st;
+    const uint8_t *head = kv.pages + (int64_t)(in ? page : 0) * kv.page_stride + head_at;
+    load_half<DP>(kv, o, head, (uint32_t)key & (kv.P() - 1u), t, st);
+  }
+  return ok;
+}
+
+// The eight codes of one dword with the scale pair {s, s} -> eight exact FP16 products.
+__device__ __forceinline__ half8_t dequant_dword(uint32_t w, half2_t sc) {
+  const half2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * sc;
+  const half2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * sc;
+  const half2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * sc;
+  const half2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * sc;
+  return half8_t{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+// Values of two keys (a, b: the same octet of each) paired for the product over keys: element
+// e of the octet as {a_e, b_e}. Swapping nibbles between the two dwords puts a_e and b_e into one
+// byte, which one conversion turns into the pair: four bit operations for sixteen elements.
+__device__ __forceinline__ uint32_t even_pairs(uint32_t a, uint32_t b) { return (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u); }
+__device__ __forceinline__ uint32_t odd_pairs(uint32_t a, uint32_t b) { return ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u); }
+
+template <int BYTE>
+__device__ __forceinline__ half2_t pair_value(uint32_t w, half2_t sc) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, BYTE) * sc;
+}
+
+__device__ __forceinline__ half8_t join4(half2_t a, half2_t b, half2_t c, half2_t d) {
+  return half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+__device__ __forceinline__ f32x4_t mfma(half8_t a, half8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Bytes of a scale dword that are NaN, as 0x80 in each; and those as 0xFF.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t s) { return ((s & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t spread(uint32_t top) { return (top >> 7) * 0xFFu; }
+
+// ------------------------------------------------------- few rows per head
+
+// Decoding and drafted tokens: up to 16 * NT rows a workgroup. The four waves take the tiles of
+// the workgroup's keys in turn, each with its own softmax state and all rows, and join at the end;
+// nothing is shared on the way, so there is no barrier in the loop. A key's and a value's bytes
+// are read once by one wave, 20 registers a tile at D = 128, the next tile's in flight while the
+// present one is computed.
+template <int DP, int NT, bool F16>
+__global__ __launch_bounds__(256) void rows_kernel(const AttnArgs A) {
+  constexpr int RT = 16 * NT, KS = Tile<DP>::KS, NB = Tile<DP>::NB, VD = Tile<DP>::VD, NU = Tile<DP>::NU;
+  constexpr int OS = DP + 4;                             // row stride of the join buffer
+  __shared__ float join_o[kWaves * 16 * OS];
+  __shared__ float join_ml[kWaves][16][2];
+  const KvView &kv = A.kv;
+  const int head = blockIdx.x % kv.heads, u = blockIdx.x / kv.heads;
+  Unit unit;
+  if (!find_unit<RT, false>(A, u, &unit)) return;
+  const Seq s = sequence<RT>(A, unit.b);
+  // (only with sequences that overlap in q_start)
+  if (unit.tile >= s.row_tiles || (unit.splits > 1 && unit.slot >= A.slots)) return;
+  const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int D = kv.D, G = A.group;
+  const int rows = min(s.queries, A.max_q) * G, row0 = unit.tile * RT;
+  const int last_row = min(rows, row0 + RT) - 1;
+
+  // keys of the tile's rows: all see [all_lo, all_hi), none sees outside [lo, hi)
+  const Range ra = keys_of(A, s, row0 / G), rb = keys_of(A, s, last_row / G);
+  const int lo = ra.lo, hi = A.mask ? s.len : rb.hi, all_lo = rb.lo, all_hi = ra.hi;
+  const int base0 = lo & ~(kTile - 1);
+  const int steps = (max(0, hi - base0) + kStep - 1) / kStep;
+  const int step0 = (int)((int64_t)steps * unit.split / unit.splits);
+  const int step1 = (int)((int64_t)steps * (unit.split + 1) / unit.splits);
+
+  // this lane's column of S^T in each row tile: its query row, scaled by a power of two
+  half8_t q[NT][KS];
+  float c[NT], ref[NT], sum[NT];
+  int klo[NT], khi[NT];
+  const uint8_t *mrow[NT];
+  const float kg = kv.k_g ? kv.k_g[head] : 1.0f;
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+    const int r = min(row0 + 16 * nt + m, last_row);
+    const int i = r / G, gh = r - i * G;
+    const Range kr = keys_of(A, s, i);
+    klo[nt] = kr.lo, khi[nt] = kr.hi;
+    mrow[nt] = A.mask ? A.mask + (int64_t)(s.first + i) * A.mask_stride : nullptr;
+    const uint16_t *src = A.q + (int64_t)(s.first + i) * A.q_t + (int64_t)(head * G + gh) * A.q_h;
+    float x[KS][8];
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KS; k++) {
+      const int d = g * (DP / 4) + 8 * k;
+      u32x4_t w = {0u, 0u, 0u, 0u};
+      if (d < D) w = *reinterpret_cast<const u32x4_t *>(src + d);
+      unpack8<F16>(w, x[k]);
+#pragma unroll
+      for (int j = 0; j < 8; j++) top = fmaxf(top, fabsf(x[k][j]));
+    }
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    // 2^e <= top < 2^(e+1); rows of zeros and rows with an infinity stay as they are
+    int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
+    if (e == 128 || top == 0.0f) e = 8;
+    e = max(e, -100);
+    const float up = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+#pragma unroll
+    for (int k = 0; k < KS; k++)
+#pragma unroll
+      for (int j = 0; j < 8; j++) q[nt][k][j] = (_Float16)(x[k][j] * up);
+    c[nt] = A.scale * 1.44269504088896f / kg * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+    ref[nt] = -INFINITY;
+    sum[nt] = 0.0f;
+  }
+  f32x4_t acc[NT][VD];
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+    for (int d = 0; d < VD; d++) acc[nt][d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const LaneOffsets off = lane_offsets<DP>(kv);
+  const int32_t *row = A.table + (int64_t)unit.b * A.table_stride;
+  const int cols = (int)(((int64_t)s.len + kv.P() - 1) >> kv.log_p);     // table entries that hold keys
+  const int64_t head_at = (int64_t)head * kv.head_bytes();
+  // scales of lanes past the head's elements are forced to zero
+  uint32_t k_keep = 0;
+#pragma unroll
+  for (int i = 0; i < NB; i++)
+    if (g * NB + i < D / 16) k_keep |= 0xFFu << (8 * i);
+  const uint32_t v_keep = m * VD < D ? 0xFFFFFFFFu : 0u;
+
+  auto compute = [&](const Tile<DP> &t, int base, uint32_t ok) {
+    const bool whole = ok == 3u && base >= all_lo && base + kTile <= all_hi;      // every row sees every key
+    // scores
+    f32x4_t st[NT][2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) st[nt][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      const uint32_t ksb = t.ks[h] & k_keep;
+#pragma unroll
+      for (int k = 0; k < KS; k++) {
+        const half2_t two = e4m3x2_to_f16(k / 2 >= 2 ? ksb >> 16 : ksb);
+        const _Float16 sc = two[(k / 2) & 1];
+        const half8_t a = dequant_dword(t.kw[h][k], half2_t{sc, sc});
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) st[nt][h] = mfma(a, q[nt][k], st[nt][h]);
+      }
+    }
+    uint32_t vs[2] = {t.vs[0] & v_keep, t.vs[1] & v_keep};
+    uint32_t nans[2] = {0u, 0u};
+    bool any_nan = false;
+    if (!whole) {
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const bool in = (ok >> h) & 1u;
+        const int key0 = base + 16 * h + 4 * g;
+        uint32_t keep = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int key = key0 + i;
+          if (in && key >= lo && key < hi) keep |= 0xFFu << (8 * i);
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            bool see = in && key >= klo[nt] && key < khi[nt];
+            if (A.mask && in && key >= khi[nt] && key < s.len) {
+              const int j = key - (s.len - s.queries);             // which new token: >= 0, as khi <= key
+              see = j < A.max_q && mrow[nt][j] != 0;
+            }
+            st[nt][h][i] = see ? st[nt][h][i] : -INFINITY;
+          }
+        }
+        // values that no row sees count as zero; NaN ones that only some rows see go another way
+        vs[h] &= keep;
+        nans[h] = nan_bytes(vs[h]);
+        vs[h] &= ~spread(nans[h]);
+      }
+      any_nan = __ballot((nans[0] | nans[1]) != 0u) != 0ull;
+    }
+    // softmax
+    half8_t p[NT];
+    half8_t seen[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      if (any_nan) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) seen[nt][j] = st[nt][j >> 2][j & 3] == -INFINITY ? (_Float16)0.0f : (_Float16)1.0f;
+      }
+      float top = fmaxf(fmaxf(fmaxf(st[nt][0][0], st[nt][0][1]), fmaxf(st[nt][0][2], st[nt][0][3])),
+                        fmaxf(fmaxf(st[nt][1][0], st[nt][1][1]), fmaxf(st[nt][1][2], st[nt][1][3])));
+      top *= c[nt];
+      if (__ballot(top > ref[nt] + kHeadroom) != 0ull) {
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float to = fmaxf(ref[nt], top);
+        const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ref[nt] - to);
+        ref[nt] = to;
+        sum[nt] *= f;
+#pragma unroll
+        for (int d = 0; d < VD; d++) acc[nt][d] *= f;
+      }
+      const float shift = kOffset - (ref[nt] == -INFINITY ? 0.0f : ref[nt]);
+      float e[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(st[nt][j >> 2][j & 3], c[nt], shift));
+        sum[nt] += e[j];
+        p[nt][j] = (_Float16)e[j];
+      }
+    }
+    // values
+    half2_t sc[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      sc[h][0] = e4m3x2_to_f16(vs[h]);
+      sc[h][1] = e4m3x2_to_f16(vs[h] >> 16);
+    }
+#pragma unroll
+    for (int u2 = 0; u2 < NU; u2++) {
+      uint32_t ev[2][2], od[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int pr = 0; pr < 2; pr++) {
+          const uint32_t wa = t.vw[h][u2][2 * pr], wb = t.vw[h][u2][2 * pr + 1];
+          ev[h][pr] = even_pairs(wa, wb);
+          od[h][pr] = odd_pairs(wa, wb);
+          if (DP == 64) {                          // half an octet per lane
+            ev[h][pr] >>= 16 * (m & 1);
+            od[h][pr] >>= 16 * (m & 1);
+          }
+        }
+#define NVFP4_KV_VALUE(B)                                                                                      \
+  if (2 * B < (DP == 64 ? 4 : 8)) {                                                                            \
+    const half8_t ve = join4(pair_value<B>(ev[0][0], sc[0][0]), pair_value<B>(ev[0][1], sc[0][1]),             \
+                             pair_value<B>(ev[1][0], sc[1][0]), pair_value<B>(ev[1][1], sc[1][1]));            \
+    const half8_t vo = join4(pair_value<B>(od[0][0], sc[0][0]), pair_value<B>(od[0][1], sc[0][1]),             \
+                             pair_value<B>(od[1][0], sc[1][0]), pair_value<B>(od[1][1], sc[1][1]));            \
+    _Pragma("unroll") for (int nt = 0; nt < NT; nt++) {                                                        \
+      acc[nt][(8 * u2 + 2 * B) % VD] = mfma(ve, p[nt], acc[nt][(8 * u2 + 2 * B) % VD]);                        \
+      acc[nt][(8 * u2 + 2 * B + 1) % VD] = mfma(vo, p[nt], acc[nt][(8 * u2 + 2 * B + 1) % VD]);                \
+    }                                                                                                          \
+  }
+      NVFP4_KV_VALUE(0) NVFP4_KV_VALUE(1) NVFP4_KV_VALUE(2) NVFP4_KV_VALUE(3)
+#undef NVFP4_KV_VALUE
+    }
+    if (any_nan) {
+      // A row that sees a NaN value gets NaN in that value's block, and no other row does: the
+      // product of "is NaN" and "is seen" counts them.
+      half8_t bad;
+#pragma unroll
+      for (int j = 0; j < 8; j++) bad[j] = (nans[j >> 2] >> (8 * (j & 3))) & 0x80u ? (_Float16)1.0f : (_Float16)0.0f;
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) {
+        const f32x4_t n = mfma(bad, seen[nt], f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+        for (int d = 0; d < VD; d++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) acc[nt][d][i] = n[i] > 0.0f ? __builtin_nanf("") : acc[nt][d][i];
+      }
+    }
+  };
+
+  // this wave's tiles: wave, wave + 4, ... of the piece
+  const int first = base0 + step0 * kStep + wave * kTile, end = min(hi, base0 + step1 * kStep);
+  if (first < end) {
+    Tile<DP> a, b;
+    uint32_t oka = load_tile<DP>(kv, off, row, cols, head_at, first, a), okb = 0;
+    for (int base = first; base < end; base += 2 * kStep) {
+      const bool more = base + kStep < end;
+      if (more) okb = load_tile<DP>(kv, off, row, cols, head_at, base + kStep, b);
+      compute(a, base, oka);
+      if (!more) break;
+      if (base + 2 * kStep < end) oka = load_tile<DP>(kv, off, row, cols, head_at, base + 2 * kStep, a);
+      compute(b, base + kStep, okb);
+    }
+  }
+
+  // join the four waves, 16 rows at a time
+  const float vg = kv.v_g ? kv.v_g[head] : 1.0f;
+  const bool final = unit.splits == 1;
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+    sum[nt] += __shfl_xor(sum[nt], 16, 64);
+    sum[nt] += __shfl_xor(sum[nt], 32, 64);
+    if (g == 0) {
+      join_ml[wave][m][0] = ref[nt];
+      join_ml[wave][m][1] = sum[nt];
+    }
+    __syncthreads();
+    float top = join_ml[0][m][0];
+#pragma unroll
+    for (int w = 1; w < kWaves; w++) top = fmaxf(top, join_ml[w][m][0]);
+    const float f = ref[nt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ref[nt] - top);
+    float *o = join_o + (wave * 16 + m) * OS + 4 * g * VD;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int d = 0; d < VD; d += 4)
+        *reinterpret_cast<f32x4_t *>(o + i * VD + d) =
+            f32x4_t{acc[nt][d][i] * f, acc[nt][d + 1][i] * f, acc[nt][d + 2][i] * f, acc[nt][d + 3][i] * f};
+    __syncthreads();
+    constexpr int PER_ROW = DP / 8;                     // threads of a row, eight elements each
+#pragma unroll
+    for (int it = threadIdx.x; it < 16 * PER_ROW; it += 256) {
+      const int n = it / PER_ROW, d = (it % PER_ROW) * 8;
+      const int r = row0 + 16 * nt + n;
+      if (r > last_row || d >= D) continue;
+      float tot = join_ml[0][n][0], l = 0.0f;
+#pragma unroll
+      for (int w = 1; w < kWaves; w++) tot = fmaxf(tot, join_ml[w][n][0]);
+      float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < kWaves; w++) {
+        const float mw = join_ml[w][n][0];
+        const float lw = join_ml[w][n][1];                 // 0 or NaN where no score was a number
+        l += mw == -INFINITY ? lw : lw * __builtin_amdgcn_exp2f(mw - tot);
+        const f32x4_t y0 = *reinterpret_cast<const f32x4_t *>(join_o + (w * 16 + n) * OS + d);
+        const f32x4_t y1 = *reinterpret_cast<const f32x4_t *>(join_o + (w * 16 + n) * OS + d + 4);
+#pragma unroll
+        for (int j = 0; j < 4; j++) x[j] += y0[j], x[j + 4] += y1[j];
+      }
+      if (final) {
+        const int i = r / G, gh = r - i * G;
+        const int64_t t = s.first + i;
+        const int h = head * G + gh;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / (l * vg);
+#pragma unroll
+        for (int j = 0; j < 8; j++) x[j] *= inv;
+        *reinterpret_cast<u32x4_t *>(A.out + t * A.o_t + h * A.o_h + d) = pack8<F16>(x);
+        if (A.lse && d == 0)
+          A.lse[t * (kv.heads * G) + h] = tot == -INFINITY && l == 0.0f
+                                              ? -INFINITY
+                                              : (tot - kOffset + __builtin_amdgcn_logf(l)) * 0.693147180559945f;
+      } else {
+        const int64_t at = ((int64_t)unit.slot * kv.heads + head) * RT + 16 * nt + n;
+        float *po = A.part_o + at * D + d;
+        *reinterpret_cast<f32x4_t *>(po) = f32x4_t{x[0], x[1], x[2], x[3]};
+        *reinterpret_cast<f32x4_t *>(po + 4) = f32x4_t{x[4], x[5], x[6], x[7]};
+        if (d == 0) {
+          A.part_ml[2 * at] = tot;
+          A.part_ml[2 * at + 1] = l;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- joining
+
+// Joins the pieces of one row of a split row tile: with m_s, l_s, O_s of piece s and m = max m_s,
+// out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s. Slices of threads take every 1024 / D-th
+// piece and are added in order, so the result does not depend on timing.
+template <int DP, int RT, bool F16>
+__global__ __launch_bounds__(256) void join_kernel(const AttnArgs A) {
+  constexpr int TH = DP / 4, SL = 256 / TH;             // threads of a slice, slices
+  __shared__ float sm_o[SL][DP];
+  __shared__ float sm_ml[SL][2];
+  const KvView &kv = A.kv;
+  const int n = blockIdx.x % RT, rest = blockIdx.x / RT;
+  const int head = rest % kv.heads, u = rest / kv.heads;
+  Unit unit;
+  if (!find_unit<RT, true>(A, u, &unit)) return;
+  const Seq s = sequence<RT>(A, unit.b);
+  if (unit.tile >= s.row_tiles || unit.slot + unit.splits > A.slots) return;
+  const int D = kv.D, G = A.group;
+  const int r = unit.tile * RT + n;
+  if (r >= min(s.queries, A.max_q) * G) return;
+  const int sl = threadIdx.x / TH, d = (threadIdx.x % TH) * 4;
+  float m = -INFINITY, l = 0.0f;
+  f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (d < D) {
+    for (int i = sl; i < unit.splits; i += SL) {
+      const int64_t at = ((int64_t)(unit.slot + i) * kv.heads + head) * RT + n;
+      const float mi = A.part_ml[2 * at], li = A.part_ml[2 * at + 1];
+      const f32x4_t oi = *reinterpret_cast<const f32x4_t *>(A.part_o + at * D + d);
+      if (mi == -INFINITY && li == 0.0f) continue;
+      const float to = fmaxf(m, mi);
+      const float fa = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - to);
+      const float fb = mi == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mi - to);
+      m = to;
+      l = l * fa + li * fb;
+      o = o * fa + oi * fb;
+    }
+    *reinterpret_cast<f32x4_t *>(&sm_o[sl][d]) = o;
+    if (d == 0) sm_ml[sl][0] = m, sm_ml[sl][1] = l;
+  }
+  __syncthreads();
+  if (sl != 0 || d >= D) return;
+  m = sm_ml[0][0];
+#pragma unroll
+  for (int i = 1; i < SL; i++) m = fmaxf(m, sm_ml[i][0]);
+  l = 0.0f;
+  o = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < SL; i++) {
+    const float mi = sm_ml[i][0], li = sm_ml[i][1];
+    if (mi == -INFINITY && li == 0.0f) continue;
+    const float f = mi == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mi - m);
+    l += li * f;
+    o += *reinterpret_cast<const f32x4_t *>(&sm_o[i][d]) * f;
+  }
+  const float vg = kv.v_g ? kv.v_g[head] : 1.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / (l * vg);
+  const int i = r / G, h = head * G + (r - i * G);
+  const int64_t t = s.first + i;
+  uint16_t *to = A.out + t * A.o_t + h * A.o_h + d;
+  const uint32_t w0 = (uint32_t)pack1<F16>(o[0] * inv) | ((uint32_t)pack1<F16>(o[1] * inv) << 16);
+  const uint32_t w1 = (uint32_t)pack1<F16>(o[2] * inv) | ((uint32_t)pack1<F16>(o[3] * inv) << 16);
+  *reinterpret_cast<u32x2_t *>(to) = u32x2_t{w0, w1};
+  if (A.lse && d == 0)
+    A.lse[t * (kv.heads * G) + h] = m == -INFINITY && l == 0.0f
+                                        ? -INFINITY
+                                        : (m - kOffset + __builtin_amdgcn_logf(l)) * 0.693147180559945f;
+}
+
+// ------------------------------------------------------------------- host
+
+// Row tiles of 16 * NT rows: as few as hold the rows of a sequence; at D > 128 the accumulators
+// of 64 rows would not fit the registers.
+static int row_tiles_of(int64_t rows, int D) {
+  const int most = D > 128 ? 2 : 4;
+  return rows <= 16 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
+}
+
+struct Launch {
+  int nt, target;
+  int64_t units, joins, slots;
+};
+
+// Sizes of a call from what the host knows of it (the lengths are on the device): pieces per KV
+// head are at most `target` + one for each row tile; row tiles that are split at most `target`,
+// with at most 2 `target` pieces together.
+static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int64_t batch, int64_t max_pages,
+                        int64_t max_q, Launch *L) {
+  const int64_t G = q_heads / kv.heads;
+  L->nt = row_tiles_of(max_q * G, kv.D);
+  const int64_t RT = 16 * L->nt;
+  const int64_t by_seq = batch * ((max_q * G + RT - 1) / RT), by_rows = total_q * G / RT + batch;
+  const int64_t tiles = by_seq < by_rows ? by_seq : by_rows;
+  L->target = kTargetWgs / kv.heads > 0 ? kTargetWgs / kv.heads : 1;
+  const int64_t steps = ((max_pages << kv.log_p) + kStep - 1) / kStep;
+  if (steps > 1) {
+    L->joins = tiles < L->target ? tiles : L->target;
+    const int64_t most = tiles * steps, slots = 2 * (int64_t)L->target;
+    L->slots = most < slots ? most : slots;
+    L->units = most < L->target + tiles ? most : L->target + tiles;
+  } else {
+    L->joins = L->slots = 0;
+    L->units = tiles;
+  }
+  return L->units * kv.heads <= 0x7FFFFFFF && L->joins * RT * kv.heads <= 0x7FFFFFFF && steps * tiles <= 0x3FFFFFFF;
+}
+
+static size_t workspace_of(const KvView &kv, const Launch &L) {
+  return (size_t)(L.slots * kv.heads * 16 * L.nt) * (kv.D + 2) * 4;
+}
+
+static nvfp4_status check_sizes(const KvView &kv, int64_t total_q, int32_t q_heads, int64_t batch, int64_t max_pages,
+                                int64_t max_q) {
+  if (q_heads < 1 || q_heads > 65535 || q_heads % kv.heads != 0) return NVFP4_ERR_SHAPE;
+  if (total_q < 0 || total_q > 0x3FFFFFFF / q_heads || batch < 0 || batch > (1 << 20) || max_q < 1 ||
+      max_q > 0x7FFFFFFF)
+    return NVFP4_ERR_SHAPE;
+  if (max_pages < 0 || max_pages > (0x7FFFFFFF >> kv.log_p) - 1) return NVFP4_ERR_SHAPE;
+  return NVFP4_OK;
+}
+
+template <int DP, int NT, bool F16>
+static void launch(const AttnArgs &A, const Launch &L, hipStream_t s) {
+  hipLaunchKernelGGL((rows_kernel<DP, NT, F16>), dim3((unsigned)(L.units * A.kv.heads)), dim3(256), 0, s, A);
+  if (L.joins)
+    hipLaunchKernelGGL((join_kernel<DP, 16 * NT, F16>), dim3((unsigned)(L.joins * A.kv.heads * 16 * NT)), dim3(256), 0, s,
+                       A);
+}
+
+template <bool F16>
+static void launch_any(const AttnArgs &A, const Launch &L, hipStream_t s) {
+  if (A.kv.D <= 64) {
+    if (L.nt == 1) launch<64, 1, F16>(A, L, s);
+    else if (L.nt == 2) launch<64, 2, F16>(A, L, s);
+    else launch<64, 4, F16>(A, L, s);
+  } else if (A.kv.D <= 128) {
+    if (L.nt == 1) launch<128, 1, F16>(A, L, s);
+    else if (L.nt == 2) launch<128, 2, F16>(A, L, s);
+    else launch<128, 4, F16>(A, L, s);
+  } else {
+    if (L.nt == 1) launch<256, 1, F16>(A, L, s);
+    else launch<256, 2, F16>(A, L, s);
+  }
+}
+
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" {
+
+size_t nvfp4_kv_attention_workspace_bytes(const nvfp4_kv_cache *cache, int64_t total_q, int32_t q_heads, int64_t batch,
+                                          int64_t max_pages, int64_t max_q) {
+  KvView kv;
+  Launch L;
+  if (kv_view(cache, &kv) != NVFP4_OK || check_sizes(kv, total_q, q_heads, batch, max_pages, max_q) != NVFP4_OK ||
+      max_q > total_q + 1 || !plan_launch(kv, total_q, q_heads, batch, max_pages, max_q, &L))
+    return 0;
+  return workspace_of(kv, L);
+}
+
+nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache *cache, nvfp4_rows q, int dtype, int64_t total_q, int32_t q_heads,
+                                const int32_t *table, int64_t table_stride, int64_t max_pages, const int32_t *lens,
+                                const int32_t *q_start, int64_t batch, int64_t max_q, const nvfp4_kv_mask *mask,
+                                nvfp4_rows out, float *lse, void *ws, size_t ws_bytes, void *stream) {
+  if (dtype != NVFP4_BF16 && dtype != NVFP4_F16) return NVFP4_ERR_DTYPE;
+  AttnArgs A = {};
+  nvfp4_status st = kv_view(cache, &A.kv);
+  if (st != NVFP4_OK) return st;
+  if ((st = check_sizes(A.kv, total_q, q_heads, batch, max_pages, max_q)) != NVFP4_OK) return st;
+  if (batch > 1 && table_stride < max_pages) return NVFP4_ERR_SHAPE;
+  if (!q_start && total_q != batch) return NVFP4_ERR_SHAPE;
+  if (!mask) return NVFP4_ERR_NULL;
+  if (!isfinite(mask->scale) || !(mask->scale > 0.0f)) return NVFP4_ERR_VALUE;
+  if ((mask->causal != 0 && mask->causal != 1) || mask->window < 0) return NVFP4_ERR_VALUE;
+  if (mask->window > 0 && (!mask->causal || mask->mask)) return NVFP4_ERR_VALUE;
+  if (mask->mask && total_q > 1 && mask->mask_stride < max_q) return NVFP4_ERR_SHAPE;
+  if (total_q == 0 || batch == 0) return NVFP4_OK;
+  if (!q.base || !out.base || !lens || (!table && max_pages > 0)) return NVFP4_ERR_NULL;
+  if (!kv_rows_aligned(q) || !kv_rows_aligned(out) || !aligned(lens, 4) || !aligned(table, 4) || !aligned(q_start, 4) ||
+      !aligned(lse, 4))
+    return NVFP4_ERR_ALIGN;
+  if (max_q > total_q) max_q = total_q;
+  Launch L;
+  if (!plan_launch(A.kv, total_q, q_heads, batch, max_pages, max_q, &L)) return NVFP4_ERR_SHAPE;
+  const size_t need = workspace_of(A.kv, L);
+  if (need > 0 && (!ws || ws_bytes < need)) return NVFP4_ERR_WORKSPACE;
+  if (need > 0 && !aligned(ws, 16)) return NVFP4_ERR_ALIGN;
+  DeviceInfo d;
+  st = device_info(&d);
+  if (st != NVFP4_OK) return st;
+  A.q = (const uint16_t *)q.base, A.q_t = q.token_stride, A.q_h = q.head_stride;
+  A.out = (uint16_t *)out.base, A.o_t = out.token_stride, A.o_h = out.head_stride;
+  A.lse = lse;
+  A.total_q = total_q;
+  A.table = table, A.table_stride = table_stride, A.max_pages = (int32_t)max_pages;
+  A.lens = lens, A.q_start = q_start;
+  A.mask = mask->mask, A.mask_stride = mask->mask_stride;
+  A.scale = mask->scale;
+  A.causal = mask->causal;
+  A.window = mask->window > 0x3FFFFFFF ? 0 : (int32_t)mask->window;
+  A.batch = (int32_t)batch, A.max_q = (int32_t)max_q;
+  A.group = q_heads / A.kv.heads;
+  A.target = L.target;
+  A.slots = (int32_t)L.slots;
+  A.part_o = (float *)ws;
+  A.part_ml = A.part_o + (L.slots * A.kv.heads * 16 * L.nt) * A.kv.D;
+  if (dtype == NVFP4_F16) launch_any<true>(A, L, (hipStream_t)stream);
+  else launch_any<false>(A, L, (hipStream_t)stream);
+  NVFP4_LAUNCH_CHECK();
+  return NVFP4_OK;
+}
+
+}  // extern "C"
