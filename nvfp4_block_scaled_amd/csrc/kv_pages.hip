@@ -393,13 +393,14 @@ __global__ __launch_bounds__(kCopyThreads) void compact_move_kernel(const Compac
     A.refs_out[A.holes[r]] = count;
     A.refs_out[from] = 0;
   }
-  if (A.refs_out == A.refs) return;
+  // (In place, a mover's count may be read before or after the loop above clears it: neither writes
+  // anything but zero there.)
   const int live = *A.live_dev;
   for (int64_t id = start; id < A.pool.num_pages; id += step) {
     const int count = A.refs[id];
     const bool alive = count > 0;
-    if (alive && id < live) A.refs_out[id] = count;          // stays
-    else if (!alive && id >= live) A.refs_out[id] = 0;       // free before and after
+    if (alive && id < live && A.refs_out != A.refs) A.refs_out[id] = count;   // stays
+    else if (!alive && id >= live) A.refs_out[id] = 0;                        // free before and after
   }
 }
 

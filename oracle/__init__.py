@@ -25,6 +25,8 @@ What is computed, with the passage each part follows:
   library, with the sign and zero folding of the block scales (TileLang PR
   #3290, "Design: Weight layout": zero scales zero their codes, negative
   scales flip code signs, prepared size N*K/2 + N*K/16).
+* ``kv``       -- the key/value cache: page layout, append with rotary positions,
+  attention in float64, page management.
 
 Everything here is deliberately slow and plain: numpy, float64 or exact
 integers, no blocking or fusion beyond what the definitions state.
