@@ -31,7 +31,7 @@ namespace nvfp4 {
 static constexpr int kWaves = 4;
 static constexpr int kTile = 32;                       // keys of one wave's step
 static constexpr int kStep = kWaves * kTile;           // keys of one workgroup's step
-static constexpr int kTargetWgs = 1024;                // workgroups that a call is split into when it has fewer
+static constexpr int kBlockRows = 128;                 // query rows of a workgroup of block_kernel
 static constexpr float kHeadroom = 8.0f;               // log2 of how far a value may pass the reference
 static constexpr float kOffset = 6.0f;                 // log2 of the factor on P
 
@@ -53,13 +53,16 @@ struct AttnArgs {
   int32_t slots;             // pieces that the workspace holds for each KV head
   float *part_o;             // workspace: partial sums [slot][row][D], then [slot][row][2] of (m, l)
   float *part_ml;
+  int32_t *join_count;       // workspace: how many row tiles are joined, and of each its first row,
+  int32_t *joins_at;         // its rows, its first slot and its pieces
+  int32_t joins;             // row tiles that the workspace has room for
 };
 
 // ------------------------------------------------------------------- plan
 
-// One sequence's share of the work; keys in steps of kStep, rows in tiles of RT.
+// One sequence's share of the work: rows in tiles of RT, keys in steps of kStep.
 struct Seq {
-  int len, queries, first;   // keys, queries computed, row of the first one
+  int len, queries, first;   // keys, queries, row of the first one
   int row_tiles, steps;      // steps: the most that one row tile has
 };
 
@@ -69,93 +72,98 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &A, int b) {
   const int64_t most = (int64_t)A.max_pages << A.kv.log_p;
   const int n = A.lens[b];
   s.len = n < 0 ? 0 : (int64_t)n > most ? (int)most : n;
-  int64_t q0 = b, q1 = b + 1;
+  int q0 = b, q1 = b + 1;
   if (A.q_start) {
-    q0 = min(max((int64_t)A.q_start[b], (int64_t)0), A.total_q);
-    q1 = min(max((int64_t)A.q_start[b + 1], q0), A.total_q);
+    const int total = (int)A.total_q;
+    q0 = min(max(A.q_start[b], 0), total);
+    q1 = min(max(A.q_start[b + 1], q0), total);
   }
-  s.first = (int)q0;
-  s.queries = (int)(q1 - q0);                 // of which the first max_q are computed
+  s.first = q0;
+  s.queries = q1 - q0;                        // of which the first max_q are computed
   const int used = min(s.queries, A.max_q);
   s.row_tiles = (used * A.group + RT - 1) / RT;
   int span = s.len;
-  if (A.window) span = (int)min((int64_t)span, (int64_t)A.window + (RT + A.group - 2) / A.group + kTile);
+  if (A.window) span = min(span, A.window + (RT + A.group - 2) / A.group + kStep / 2);
   s.steps = (span + kStep - 1) / kStep;
   return s;
 }
 
-__device__ __forceinline__ int wave_sum_scan(int v) {   // inclusive
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int y = __shfl_up(v, off, 64);
-    if (lane >= off) v += y;
-  }
+// Inclusive prefix sum over a wave: shifts inside rows of 16 lanes, then the rows' last lanes.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31 into rows 2 and 3
   return v;
 }
+
+__device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
 
 // A workgroup's unit: one row tile of one sequence, and one of the `splits` pieces of its keys.
 struct Unit {
   int b, tile, split, splits, slot;
+  Seq s;
 };
 
-__device__ __forceinline__ int splits_of(const Seq &s, int chunk) { return max(1, (s.steps + chunk - 1) / chunk); }
-
-// Steps a piece may have: the whole call's steps over the workgroups to fill.
-template <int RT>
-__device__ __forceinline__ int chunk_steps(const AttnArgs &A) {
-  int total = 0;
-  for (int base = 0; base < A.batch; base += 64) {
-    const int b = base + (threadIdx.x & 63);
-    int w = 0;
-    if (b < A.batch) {
-      const Seq s = sequence<RT>(A, b);
-      w = s.row_tiles * s.steps;
-    }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) w += __shfl_xor(w, off, 64);
-    total += w;
+// Finds unit `u`; false past the last. Every wave does it for itself, a lane per sequence, with no
+// exchange through memory: pieces are as long as the call's steps over the workgroups to fill, and
+// a prefix sum over the sequences' pieces says whose piece `u` is. The first workgroup of each
+// split row tile leaves what join_kernel has to know of it. REVERSE: of a sequence under the causal
+// mask, the last row tile comes first: it sees the most keys.
+template <int RT, bool REVERSE>
+__device__ __forceinline__ bool find_unit(const AttnArgs &A, int u, bool tell, Unit *out) {
+  const int lane = threadIdx.x & 63;
+  const Seq none = {0, 0, 0, 0, 0};
+  const Seq s0 = lane < A.batch ? sequence<RT>(A, lane) : none;
+  int total = last_lane(wave_scan(s0.row_tiles * s0.steps));
+  for (int base = 64; base < A.batch; base += 64) {
+    const Seq s = base + lane < A.batch ? sequence<RT>(A, base + lane) : none;
+    total += last_lane(wave_scan(s.row_tiles * s.steps));
   }
-  return max(1, (total + A.target - 1) / A.target);
-}
-
-// Finds unit `u` (COMBINE: split row tile `u`); false past the last. Every wave does it for itself.
-template <int RT, bool COMBINE>
-__device__ __forceinline__ bool find_unit(const AttnArgs &A, int u, Unit *out) {
-  const int chunk = chunk_steps<RT>(A);
-  int units = 0, slots = 0;
+  const int chunk = max(1, (total + A.target - 1) / A.target);
+  int units = 0, slots = 0, joins = 0;
+  bool found = false;
   for (int base = 0; base < A.batch; base += 64) {
-    const int b = base + (threadIdx.x & 63);
-    int mine = 0, part = 0, splits = 1;
-    if (b < A.batch) {
-      const Seq s = sequence<RT>(A, b);
-      splits = splits_of(s, chunk);
-      mine = COMBINE ? (splits > 1 ? s.row_tiles : 0) : s.row_tiles * splits;
-      part = splits > 1 ? s.row_tiles * splits : 0;
-    }
-    const int to = units + wave_sum_scan(mine), slot_to = slots + wave_sum_scan(part);
+    const Seq s = base == 0 ? s0 : base + lane < A.batch ? sequence<RT>(A, base + lane) : none;
+    const int n = max(1, (s.steps + chunk - 1) / chunk);
+    const int mine = s.row_tiles * n, part = n > 1 ? mine : 0, join = n > 1 ? s.row_tiles : 0;
+    const int to = units + wave_scan(mine), slot_to = slots + wave_scan(part), join_to = joins + wave_scan(join);
     const uint64_t hit = __ballot(u < to);
-    if (hit) {
-      const int lane = __builtin_ctzll(hit);
-      const int first = __builtin_amdgcn_readlane(to - mine, lane);
-      const int slot = __builtin_amdgcn_readlane(slot_to - part, lane);
-      const int n = __builtin_amdgcn_readlane(splits, lane);
-      out->b = base + lane;
-      out->splits = n;
-      if (COMBINE) {
-        out->tile = u - first;
-        out->split = 0;
-      } else {
-        out->tile = (u - first) / n;
-        out->split = (u - first) - out->tile * n;
+    if (hit && !found) {
+      found = true;
+      const int at = __builtin_ctzll(hit);
+      const int first = __builtin_amdgcn_readlane(to - mine, at);
+      out->b = base + at;
+      out->splits = __builtin_amdgcn_readlane(n, at);
+      out->tile = (u - first) / out->splits;
+      out->split = (u - first) - out->tile * out->splits;
+      out->slot = __builtin_amdgcn_readlane(slot_to - part, at) + u - first;
+      out->s.len = __builtin_amdgcn_readlane(s.len, at);
+      out->s.queries = __builtin_amdgcn_readlane(s.queries, at);
+      out->s.first = __builtin_amdgcn_readlane(s.first, at);
+      out->s.row_tiles = __builtin_amdgcn_readlane(s.row_tiles, at);
+      out->s.steps = __builtin_amdgcn_readlane(s.steps, at);
+      const int tile = out->tile;
+      if (REVERSE && A.causal) out->tile = out->s.row_tiles - 1 - tile;
+      if (tell && out->splits > 1 && out->split == 0) {
+        const int j = __builtin_amdgcn_readlane(join_to - join, at) + tile;
+        if (j < A.joins && threadIdx.x == 0) {
+          const int rows = min(out->s.queries, A.max_q) * A.group - out->tile * RT;
+          A.joins_at[4 * j] = out->s.first * A.group + out->tile * RT;       // (query, head of the group) row
+          A.joins_at[4 * j + 1] = min(rows, RT);
+          A.joins_at[4 * j + 2] = out->slot;
+          A.joins_at[4 * j + 3] = out->splits;
+        }
       }
-      out->slot = slot + out->tile * n + out->split;
-      return true;
+      if (!tell || u != 0) return true;
     }
-    units = __builtin_amdgcn_readlane(to, 63);
-    slots = __builtin_amdgcn_readlane(slot_to, 63);
+    units = last_lane(to), slots = last_lane(slot_to), joins = last_lane(join_to);
   }
-  return false;
+  // how many row tiles are to be joined (the first workgroup of the grid)
+  if (tell && u == 0 && threadIdx.x == 0) *A.join_count = joins;
+  return found;
 }
 
 // The keys that query i of a sequence sees: [lo, hi) (under a tree mask, those before the new ones).
@@ -301,6 +309,16 @@ __device__ __forceinline__ f32x4_t mfma(half8_t a, half8_t b, f32x4_t c) {
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t s) { return ((s & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ uint32_t spread(uint32_t top) { return (top >> 7) * 0xFFu; }
 
+// The power of two that brings a query row with largest magnitude `top` into [2^8, 2^9), and its
+// inverse (returned). Rows of zeros and rows with an infinity stay as they are.
+__device__ __forceinline__ float query_scale(float top, float *up) {
+  int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;      // 2^e <= top < 2^(e+1)
+  if (e == 128 || top == 0.0f) e = 8;
+  e = max(e, -100);
+  *up = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+  return __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+}
+
 // ------------------------------------------------------- few rows per head
 
 // Decoding and drafted tokens: up to 16 * NT rows a workgroup. The four waves take the tiles of
@@ -309,7 +327,7 @@ __device__ __forceinline__ uint32_t spread(uint32_t top) { return (top >> 7) * 0
 // are read once by one wave, 20 registers a tile at D = 128, the next tile's in flight while the
 // present one is computed.
 template <int DP, int NT, bool F16>
-__global__ __launch_bounds__(256) void rows_kernel(const AttnArgs A) {
+__global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 4 : 2) void rows_kernel(const AttnArgs A) {
   constexpr int RT = 16 * NT, KS = Tile<DP>::KS, NB = Tile<DP>::NB, VD = Tile<DP>::VD, NU = Tile<DP>::NU;
   constexpr int OS = DP + 4;                             // row stride of the join buffer
   __shared__ float join_o[kWaves * 16 * OS];
@@ -317,10 +335,10 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnArgs A) {
   const KvView &kv = A.kv;
   const int head = blockIdx.x % kv.heads, u = blockIdx.x / kv.heads;
   Unit unit;
-  if (!find_unit<RT, false>(A, u, &unit)) return;
-  const Seq s = sequence<RT>(A, unit.b);
+  if (!find_unit<RT, false>(A, u, A.joins > 0 && head == 0, &unit)) return;
+  const Seq &s = unit.s;
   // (only with sequences that overlap in q_start)
-  if (unit.tile >= s.row_tiles || (unit.splits > 1 && unit.slot >= A.slots)) return;
+  if (unit.tile < 0 || unit.tile >= s.row_tiles || (unit.splits > 1 && unit.slot >= A.slots)) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int D = kv.D, G = A.group;
@@ -362,16 +380,12 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnArgs A) {
     }
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
-    // 2^e <= top < 2^(e+1); rows of zeros and rows with an infinity stay as they are
-    int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
-    if (e == 128 || top == 0.0f) e = 8;
-    e = max(e, -100);
-    const float up = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+    float up;
+    c[nt] = A.scale * 1.44269504088896f / kg * query_scale(top, &up);
 #pragma unroll
     for (int k = 0; k < KS; k++)
 #pragma unroll
       for (int j = 0; j < 8; j++) q[nt][k][j] = (_Float16)(x[k][j] * up);
-    c[nt] = A.scale * 1.44269504088896f / kg * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
     ref[nt] = -INFINITY;
     sum[nt] = 0.0f;
   }
@@ -610,64 +624,440 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnArgs A) {
   }
 }
 
+// ------------------------------------------------------ many rows per head
+
+// Prefill chunks and larger sets of drafted tokens: 128 rows a workgroup, 32 a wave, in 32 x 32 x 16
+// steps. What rows_kernel does for each wave, dequantizing, the four waves do together here: a tile
+// of KT keys goes once to LDS as FP16, already in the order in which the matrix cores take it (a
+// fragment of 64 lanes x 16 bytes is contiguous: neither writes nor reads conflict), and every wave
+// reads all of it. Two tiles are kept: while one is multiplied, the next one's codes are on their
+// way into registers, and they are dequantized into the other buffer before the one barrier of a
+// tile.
+template <int DP>
+struct Block {
+  static constexpr int KT = DP == 256 ? 32 : 64;       // keys of a tile (LDS: 64 KiB at D >= 128)
+  static constexpr int KG = KT / 32;                   // 32-key rows of S^T
+  static constexpr int KS = DP / 16;                   // products of 16 along a key's elements
+  static constexpr int PARTS = DP / 64;                // 32-element parts of a half key
+  static constexpr int DT = DP / 32;                   // 32-element columns of V
+  static constexpr int T16 = KT / 16;                  // products of 16 along the keys
+  static constexpr int OCTETS = DP / 8;
+  static constexpr int K_WAVES = KG * PARTS;           // waves that dequantize keys: 2, 4, 4
+  static constexpr int V_FIRST = DP == 64 ? 2 : 0;     // first wave that dequantizes values
+};
+
+__device__ __forceinline__ f32x16_t mfma32(half8_t a, half8_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// A thread's part of a tile as it lies in the cache: 32 elements of one key, eight of four values.
+struct Raw {
+  u32x4_t kw, vw;
+  uint32_t ks, vs;
+};
+
+template <int DP, bool F16>
+__global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
+  using B = Block<DP>;
+  constexpr int RT = kBlockRows, KT = B::KT, KG = B::KG, KS = B::KS, DT = B::DT, T16 = B::T16;
+  __shared__ u32x4_t kbuf[2][KG * KS * 64];
+  __shared__ u32x4_t vbuf[2][DT * T16 * 64];
+  const KvView &kv = A.kv;
+  const int head = blockIdx.x % kv.heads, u = blockIdx.x / kv.heads;
+  Unit unit;
+  if (!find_unit<RT, true>(A, u, A.joins > 0 && head == 0, &unit)) return;
+  const Seq &s = unit.s;
+  if (unit.tile < 0 || unit.tile >= s.row_tiles || (unit.splits > 1 && unit.slot >= A.slots)) return;
+  const int lane = threadIdx.x & 63, m = lane & 31, hi = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int D = kv.D, G = A.group;
+  const int rows = min(s.queries, A.max_q) * G, row0 = unit.tile * RT, last_row = min(rows, row0 + RT) - 1;
+  const Range ra = keys_of(A, s, row0 / G), rb = keys_of(A, s, last_row / G);
+  const int lo = ra.lo, end = A.mask ? s.len : rb.hi, all_lo = rb.lo, all_hi = ra.hi;
+  // this wave's rows (the last ones again where there are fewer)
+  const int w0 = min(row0 + 32 * wave, last_row), w1 = min(row0 + 32 * wave + 31, last_row);
+  const bool working = row0 + 32 * wave <= last_row;
+  const Range wa = keys_of(A, s, w0 / G), wb = keys_of(A, s, w1 / G);
+  const int w_lo = wa.lo, w_hi = A.mask ? s.len : wb.hi;
+  const int base0 = lo & ~(kStep - 1);
+  const int steps = (max(0, end - base0) + kStep - 1) / kStep;
+  const int first = base0 + (int)((int64_t)steps * unit.split / unit.splits) * kStep;
+  const int last = min(end, base0 + (int)((int64_t)steps * (unit.split + 1) / unit.splits) * kStep);
+
+  // this lane's column of S^T: its query row, scaled by a power of two
+  const int r = min(row0 + 32 * wave + m, last_row);
+  const int qi = r / G, gh = r - qi * G;
+  const Range mine = keys_of(A, s, qi);
+  const uint8_t *mrow = A.mask ? A.mask + (int64_t)(s.first + qi) * A.mask_stride : nullptr;
+  half8_t q[KS];
+  float c;
+  {
+    const uint16_t *src = A.q + (int64_t)(s.first + qi) * A.q_t + (int64_t)(head * G + gh) * A.q_h;
+    u32x4_t w[KS];
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KS; k++) {
+      const int d = hi * (DP / 2) + 8 * k;
+      w[k] = u32x4_t{0u, 0u, 0u, 0u};
+      if (d < D) w[k] = *reinterpret_cast<const u32x4_t *>(src + d);
+    }
+#pragma unroll
+    for (int k = 0; k < KS; k++) {
+      float x[8];
+      unpack8<F16>(w[k], x);
+#pragma unroll
+      for (int j = 0; j < 8; j++) top = fmaxf(top, fabsf(x[j]));
+    }
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    float up;
+    c = A.scale * 1.44269504088896f / (kv.k_g ? kv.k_g[head] : 1.0f) * query_scale(top, &up);
+#pragma unroll
+    for (int k = 0; k < KS; k++) {
+      float x[8];
+      unpack8<F16>(w[k], x);
+#pragma unroll
+      for (int j = 0; j < 8; j++) q[k][j] = (_Float16)(x[j] * up);
+    }
+  }
+
+  // which part of a tile this thread dequantizes
+  const bool k_task = wave < B::K_WAVES, v_task = wave >= B::V_FIRST;
+  const int kg = k_task ? wave / B::PARTS : 0, part = k_task ? wave % B::PARTS : 0;
+  const int kd0 = hi * (DP / 2) + part * 32;             // first element of its key part
+  const int vw = wave - B::V_FIRST;
+  const int octet = DP == 64 ? lane & 7 : DP == 128 ? lane & 15 : (lane & 15) + 16 * (vw & 1);
+  const int tg = DP == 64 ? vw * 8 + (lane >> 3) : DP == 128 ? vw * 4 + (lane >> 4) : (vw >> 1) * 4 + (lane >> 4);
+  const uint32_t octets = D / 8, blocks = D / 16;
+  const uint32_t oc = min((uint32_t)octet, octets - 1);
+  const uint32_t k_keep = (kd0 < D ? 0xFFu : 0u) | (kd0 + 16 < D ? 0xFF00u : 0u);
+  const uint32_t v_keep = 8 * octet < D ? 0xFFFFFFFFu : 0u;
+  const int32_t *row = A.table + (int64_t)unit.b * A.table_stride;
+  const int cols = (int)(((int64_t)s.len + kv.P() - 1) >> kv.log_p);     // table entries that hold keys
+  const int64_t head_at = (int64_t)head * kv.head_bytes();
+  // (a key row may be overrun inside its page, as in lane_offsets; the scale pair of a part past the
+  // head's elements is taken from the last two bytes)
+  const uint32_t k_off = kd0 / 2, ks_off = kv.k_scales() + (blocks < 2 ? 0u : min((uint32_t)kd0 / 16, blocks - 1));
+  const uint32_t v_off = kv.v_codes() + oc * 16, vs_off = kv.v_scales() + ((oc / 2) << kv.log_p);
+
+  // page ids of a tile's groups of 16 keys, one lane each
+  auto load_ids = [&](int base) {
+    const int col = (base + 16 * lane) >> kv.log_p;
+    return lane < T16 && col < cols ? row[col] : -1;
+  };
+  auto page_at = [&](int ids, int group) {
+    const int id = __builtin_amdgcn_readlane(ids, group);
+    return kv.pages + (int64_t)(id >= 0 && id < kv.num_pages ? id : 0) * kv.page_stride + head_at;
+  };
+  auto load_raw = [&](int ids, int base, Raw &t) {
+    if (k_task) {
+      const int key = base + 32 * kg + m;
+      const uint8_t *p0 = page_at(ids, 2 * kg), *p1 = page_at(ids, 2 * kg + 1);
+      const uint8_t *p = m < 16 ? p0 : p1;
+      const uint32_t at = (uint32_t)key & (kv.P() - 1u);
+      t.kw = *reinterpret_cast<const u32x4_a4 *>(p + at * (uint32_t)(D / 2) + k_off);
+      t.ks = load_bytes<2>(p + at * blocks + ks_off);
+    }
+    if (v_task) {
+      const int token = base + 4 * tg;
+      const uint8_t *p = DP == 64 ? ((tg >> 2) & 1 ? page_at(ids, 2 * vw + 1) : page_at(ids, 2 * vw))
+                                  : page_at(ids, DP == 128 ? vw : vw >> 1);
+      const uint32_t at = (uint32_t)token & (kv.P() - 1u);
+      t.vw = *reinterpret_cast<const u32x4_t *>(p + at * (uint32_t)(D / 2) + v_off);
+      t.vs = *reinterpret_cast<const uint32_t *>(p + at + vs_off);
+    }
+  };
+  // Dequantizes this thread's part into buffer `buf`; true if it met a NaN value that some rows may
+  // not see (its scale then counts as zero: see nan_rows).
+  auto store_tile = [&](const Raw &t, int base, int buf) {
+    bool nan = false;
+    if (k_task) {
+      const half2_t sc = e4m3x2_to_f16(t.ks & k_keep);
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const _Float16 f = sc[i >> 1];
+        const half8_t w = dequant_dword(t.kw[i], half2_t{f, f});
+        u32x4_t o;
+        __builtin_memcpy(&o, &w, 16);
+        kbuf[buf][(kg * KS + 4 * part + i) * 64 + lane] = o;
+      }
+    }
+    if (v_task) {
+      uint32_t vs = t.vs & v_keep;
+      if (base < all_lo || base + KT > all_hi) {
+        uint32_t keep = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int key = base + 4 * tg + i;
+          if (key >= lo && key < end) keep |= 0xFFu << (8 * i);
+        }
+        vs &= keep;
+        const uint32_t bad = nan_bytes(vs);
+        vs &= ~spread(bad);
+        nan = bad != 0u;
+      }
+      const half2_t s01 = e4m3x2_to_f16(vs), s23 = e4m3x2_to_f16(vs >> 16);
+      const uint32_t e01 = even_pairs(t.vw[0], t.vw[1]), o01 = odd_pairs(t.vw[0], t.vw[1]);
+      const uint32_t e23 = even_pairs(t.vw[2], t.vw[3]), o23 = odd_pairs(t.vw[2], t.vw[3]);
+      // element e of the octet: column e % DT, lane octet + OCTETS * (e / DT); four tokens are half
+      // of the eight that a lane holds, the other half and the other half wave by the token group
+      uint8_t *to = reinterpret_cast<uint8_t *>(vbuf[buf]) + ((tg >> 2) * 64 + (tg & 1) * 32 + octet) * 16 + ((tg >> 1) & 1) * 8;
+#define NVFP4_KV_PUT(E, X, Y)                                                                             \
+  {                                                                                                       \
+    const half2_t a = X, b = Y;                                                                           \
+    const uint32_t ua = __builtin_bit_cast(uint32_t, a), ub = __builtin_bit_cast(uint32_t, b);            \
+    *reinterpret_cast<u32x2_t *>(to + ((E % DT) * T16 * 64 + B::OCTETS * (E / DT)) * 16) = u32x2_t{ua, ub}; \
+  }
+      NVFP4_KV_PUT(0, pair_value<0>(e01, s01), pair_value<0>(e23, s23))
+      NVFP4_KV_PUT(1, pair_value<0>(o01, s01), pair_value<0>(o23, s23))
+      NVFP4_KV_PUT(2, pair_value<1>(e01, s01), pair_value<1>(e23, s23))
+      NVFP4_KV_PUT(3, pair_value<1>(o01, s01), pair_value<1>(o23, s23))
+      NVFP4_KV_PUT(4, pair_value<2>(e01, s01), pair_value<2>(e23, s23))
+      NVFP4_KV_PUT(5, pair_value<2>(o01, s01), pair_value<2>(o23, s23))
+      NVFP4_KV_PUT(6, pair_value<3>(e01, s01), pair_value<3>(e23, s23))
+      NVFP4_KV_PUT(7, pair_value<3>(o01, s01), pair_value<3>(o23, s23))
+#undef NVFP4_KV_PUT
+    }
+    return nan;
+  };
+
+  float ref = -INFINITY, sum = 0.0f;
+  f32x16_t acc[DT];
+#pragma unroll
+  for (int d = 0; d < DT; d++)
+#pragma unroll
+    for (int i = 0; i < 16; i++) acc[d][i] = 0.0f;
+
+  bool nan_now = false, nan_next = false;
+  int ids = 0, ids_next = 0;
+  Raw raw = {};
+  if (first < last) {
+    ids = load_ids(first);
+    load_raw(ids, first, raw);
+    ids_next = load_ids(first + KT);
+    nan_now = store_tile(raw, first, 0);
+  }
+  nan_now = __syncthreads_or(nan_now);
+  int buf = 0;
+  for (int base = first; base < last; base += KT, buf ^= 1) {
+    const bool more = base + KT < last;
+    int ids_after = 0;
+    if (more) {
+      load_raw(ids_next, base + KT, raw);
+      ids_after = load_ids(base + 2 * KT);
+    }
+    if (working && base < w_hi && base + KT > w_lo) {
+      f32x16_t st[KG];
+#pragma unroll
+      for (int g = 0; g < KG; g++) {
+#pragma unroll
+        for (int i = 0; i < 16; i++) st[g][i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+          const u32x4_t w = kbuf[buf][(g * KS + k) * 64 + lane];
+          half8_t a;
+          __builtin_memcpy(&a, &w, 16);
+          st[g] = mfma32(a, q[k], st[g]);
+        }
+      }
+      const uint32_t ok = (uint32_t)__ballot(ids >= 0 && ids < kv.num_pages) & ((1u << T16) - 1u);
+      const bool whole = ok == (1u << T16) - 1u && base >= wb.lo && base + KT <= wa.hi;
+      if (!whole) {
+#pragma unroll
+        for (int g = 0; g < KG; g++)
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            const int key = base + 32 * g + 8 * (i >> 2) + 4 * hi + (i & 3);
+            const bool in = (ok >> (2 * g + (i >> 3))) & 1u;
+            bool see = in && key >= mine.lo && key < mine.hi;
+            if (A.mask && in && key >= mine.hi && key < s.len) {
+              const int j = key - (s.len - s.queries);
+              see = j < A.max_q && mrow[j] != 0;
+            }
+            st[g][i] = see ? st[g][i] : -INFINITY;
+          }
+      }
+      float top = st[0][0];
+#pragma unroll
+      for (int g = 0; g < KG; g++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) top = fmaxf(top, st[g][i]);
+      top *= c;
+      if (__ballot(top > ref + kHeadroom) != 0ull) {
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float to = fmaxf(ref, top);
+        const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ref - to);
+        ref = to;
+        sum *= f;
+#pragma unroll
+        for (int d = 0; d < DT; d++)
+#pragma unroll
+          for (int i = 0; i < 16; i++) acc[d][i] *= f;
+      }
+      const float shift = kOffset - (ref == -INFINITY ? 0.0f : ref);
+#pragma unroll
+      for (int t = 0; t < T16; t++) {
+        half8_t p, seen;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          const float x = st[t >> 1][8 * (t & 1) + j];
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x, c, shift));
+          sum += e;
+          p[j] = (_Float16)e;
+          if (nan_now) seen[j] = x == -INFINITY ? (_Float16)0.0f : (_Float16)1.0f;
+        }
+#pragma unroll
+        for (int d = 0; d < DT; d++) {
+          const u32x4_t w = vbuf[buf][(d * T16 + t) * 64 + lane];
+          half8_t a;
+          __builtin_memcpy(&a, &w, 16);
+          acc[d] = mfma32(a, p, acc[d]);
+        }
+        if (nan_now) {
+          // A row that sees a NaN value gets NaN in that value's block, and no other row does: the
+          // product of "is NaN" and "is seen" counts them. (All of a lane's elements lie in a block.)
+          const uint8_t *page = page_at(ids, t);
+          const uint32_t at = (uint32_t)(base + 16 * t + 4 * hi) & (kv.P() - 1u);
+          const uint32_t blk = min((uint32_t)(m % B::OCTETS) / 2, blocks - 1);
+          half8_t bad;
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            const uint32_t vs = page[kv.v_scales() + (blk << kv.log_p) + at + 8 * (j >> 2) + (j & 3)];
+            bad[j] = (vs & 0x7Fu) == 0x7Fu && (ok >> t) & 1u ? (_Float16)1.0f : (_Float16)0.0f;
+          }
+          f32x16_t n;
+#pragma unroll
+          for (int i = 0; i < 16; i++) n[i] = 0.0f;
+          n = mfma32(bad, seen, n);
+#pragma unroll
+          for (int d = 0; d < DT; d++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) acc[d][i] = n[i] > 0.0f ? __builtin_nanf("") : acc[d][i];
+        }
+      }
+    }
+    if (more) nan_next = store_tile(raw, base + KT, buf ^ 1);
+    // (only tiles that some rows see in part look at values one by one)
+    if (more && (base + KT < all_lo || base + 2 * KT > all_hi)) nan_now = __syncthreads_or(nan_next);
+    else {
+      __syncthreads();
+      nan_now = false;
+    }
+    ids = ids_next;
+    ids_next = ids_after;
+  }
+  if (!working) return;
+
+  sum += __shfl_xor(sum, 32, 64);
+  const float vg = kv.v_g ? kv.v_g[head] : 1.0f;
+  const bool final = unit.splits == 1;
+  if (row0 + 32 * wave + m > last_row) return;
+  // element d of column dt in register i: see store_tile for which it is
+  if (final) {
+    const int64_t t = s.first + qi;
+    const int h = head * G + gh;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / (sum * vg);
+    uint16_t *out = A.out + t * A.o_t + h * A.o_h;
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      const int mm = 8 * (i >> 2) + 4 * hi + (i & 3);
+      const int d = 8 * (mm % B::OCTETS) + DT * (mm / B::OCTETS);
+      if (d >= D) continue;
+#pragma unroll
+      for (int j = 0; j < DT; j += 2) {
+        const uint32_t w = (uint32_t)pack1<F16>(acc[j][i] * inv) | ((uint32_t)pack1<F16>(acc[j + 1][i] * inv) << 16);
+        *reinterpret_cast<uint32_t *>(out + d + j) = w;
+      }
+    }
+    if (A.lse && hi == 0)
+      A.lse[t * (kv.heads * G) + h] = ref == -INFINITY && sum == 0.0f
+                                          ? -INFINITY
+                                          : (ref - kOffset + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
+  } else {
+    const int64_t at = ((int64_t)unit.slot * kv.heads + head) * RT + 32 * wave + m;
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      const int mm = 8 * (i >> 2) + 4 * hi + (i & 3);
+      const int d = 8 * (mm % B::OCTETS) + DT * (mm / B::OCTETS);
+      if (d >= D) continue;
+#pragma unroll
+      for (int j = 0; j < DT; j += 2) *reinterpret_cast<f32x2_t *>(A.part_o + at * D + d + j) = f32x2_t{acc[j][i], acc[j + 1][i]};
+    }
+    if (hi == 0) A.part_ml[2 * at] = ref, A.part_ml[2 * at + 1] = sum;
+  }
+}
+
 // ---------------------------------------------------------------- joining
 
-// Joins the pieces of one row of a split row tile: with m_s, l_s, O_s of piece s and m = max m_s,
-// out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s. Slices of threads take every 1024 / D-th
-// piece and are added in order, so the result does not depend on timing.
-template <int DP, int RT, bool F16>
+// Joins the pieces of a split row tile: with m_s, l_s, O_s of piece s and m = max m_s,
+// out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s. DP / 4 threads hold a row (four elements
+// each) and are a slice; ROWS rows share a workgroup, and the slices of a row take its pieces in
+// turn, eight loads in flight, and are added in order: the result does not depend on timing.
+template <int DP, int RT, int ROWS, bool F16>
 __global__ __launch_bounds__(256) void join_kernel(const AttnArgs A) {
-  constexpr int TH = DP / 4, SL = 256 / TH;             // threads of a slice, slices
-  __shared__ float sm_o[SL][DP];
-  __shared__ float sm_ml[SL][2];
+  constexpr int TH = DP / 4, SL = 256 / TH / ROWS;      // threads of a slice, slices of a row
+  static_assert(SL >= 1, "too many rows");
+  __shared__ f32x4_t sm_o[ROWS * SL * TH];
+  __shared__ float sm_ml[ROWS * SL][2];
   const KvView &kv = A.kv;
-  const int n = blockIdx.x % RT, rest = blockIdx.x / RT;
-  const int head = rest % kv.heads, u = rest / kv.heads;
-  Unit unit;
-  if (!find_unit<RT, true>(A, u, &unit)) return;
-  const Seq s = sequence<RT>(A, unit.b);
-  if (unit.tile >= s.row_tiles || unit.slot + unit.splits > A.slots) return;
+  const int group = blockIdx.x % (RT / ROWS), rest = blockIdx.x / (RT / ROWS);
+  const int head = rest % kv.heads, j = rest / kv.heads;
+  if (j >= *A.join_count) return;
+  const int row0 = A.joins_at[4 * j], rows = A.joins_at[4 * j + 1], slot = A.joins_at[4 * j + 2], splits = A.joins_at[4 * j + 3];
+  if (group * ROWS >= rows || slot + splits > A.slots) return;
   const int D = kv.D, G = A.group;
-  const int r = unit.tile * RT + n;
-  if (r >= min(s.queries, A.max_q) * G) return;
   const int sl = threadIdx.x / TH, d = (threadIdx.x % TH) * 4;
+  const int n = group * ROWS + sl / SL, part = sl % SL;
   float m = -INFINITY, l = 0.0f;
   f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (d < D) {
-    for (int i = sl; i < unit.splits; i += SL) {
-      const int64_t at = ((int64_t)(unit.slot + i) * kv.heads + head) * RT + n;
-      const float mi = A.part_ml[2 * at], li = A.part_ml[2 * at + 1];
-      const f32x4_t oi = *reinterpret_cast<const f32x4_t *>(A.part_o + at * D + d);
-      if (mi == -INFINITY && li == 0.0f) continue;
-      const float to = fmaxf(m, mi);
-      const float fa = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - to);
-      const float fb = mi == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mi - to);
-      m = to;
-      l = l * fa + li * fb;
-      o = o * fa + oi * fb;
+  if (d < D && n < rows) {
+    const int64_t at0 = ((int64_t)slot * kv.heads + head) * RT + n, step = (int64_t)kv.heads * RT;
+    for (int i0 = part; i0 < splits; i0 += 8 * SL) {
+      float mi[8], li[8];
+      f32x4_t oi[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const int piece = i0 + i * SL;
+        const int64_t at = at0 + min(piece, splits - 1) * step;
+        const f32x2_t ml = *reinterpret_cast<const f32x2_t *>(A.part_ml + 2 * at);
+        oi[i] = *reinterpret_cast<const f32x4_t *>(A.part_o + at * D + d);
+        mi[i] = piece < splits ? ml[0] : -INFINITY;
+        li[i] = piece < splits ? ml[1] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        if (mi[i] == -INFINITY && li[i] == 0.0f) continue;         // a piece without keys
+        const float to = fmaxf(m, mi[i]);
+        const float fa = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+        const float fb = mi[i] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mi[i] - to);
+        m = to;
+        l = l * fa + li[i] * fb;
+        o = o * fa + oi[i] * fb;
+      }
     }
-    *reinterpret_cast<f32x4_t *>(&sm_o[sl][d]) = o;
+  }
+  if (SL > 1) {
+    sm_o[threadIdx.x] = o;
     if (d == 0) sm_ml[sl][0] = m, sm_ml[sl][1] = l;
-  }
-  __syncthreads();
-  if (sl != 0 || d >= D) return;
-  m = sm_ml[0][0];
+    __syncthreads();
+    if (part == 0) {
 #pragma unroll
-  for (int i = 1; i < SL; i++) m = fmaxf(m, sm_ml[i][0]);
-  l = 0.0f;
-  o = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < SL; i++) {
-    const float mi = sm_ml[i][0], li = sm_ml[i][1];
-    if (mi == -INFINITY && li == 0.0f) continue;
-    const float f = mi == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mi - m);
-    l += li * f;
-    o += *reinterpret_cast<const f32x4_t *>(&sm_o[i][d]) * f;
+      for (int i = 1; i < SL; i++) {
+        const float mi = sm_ml[sl + i][0], li = sm_ml[sl + i][1];
+        if (mi == -INFINITY && li == 0.0f) continue;
+        const float to = fmaxf(m, mi);
+        const float fa = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+        const float fb = mi == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mi - to);
+        m = to;
+        l = l * fa + li * fb;
+        o = o * fa + sm_o[threadIdx.x + i * TH] * fb;
+      }
+    }
   }
+  if (part != 0 || d >= D || n >= rows) return;
   const float vg = kv.v_g ? kv.v_g[head] : 1.0f;
   const float inv = l == 0.0f ? 0.0f : 1.0f / (l * vg);
-  const int i = r / G, h = head * G + (r - i * G);
-  const int64_t t = s.first + i;
+  const int r = row0 + n, h = head * G + r % G;
+  const int64_t t = r / G;
   uint16_t *to = A.out + t * A.o_t + h * A.o_h + d;
   const uint32_t w0 = (uint32_t)pack1<F16>(o[0] * inv) | ((uint32_t)pack1<F16>(o[1] * inv) << 16);
   const uint32_t w1 = (uint32_t)pack1<F16>(o[2] * inv) | ((uint32_t)pack1<F16>(o[3] * inv) << 16);
@@ -680,15 +1070,9 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs A) {
 
 // ------------------------------------------------------------------- host
 
-// Row tiles of 16 * NT rows: as few as hold the rows of a sequence; at D > 128 the accumulators
-// of 64 rows would not fit the registers.
-static int row_tiles_of(int64_t rows, int D) {
-  const int most = D > 128 ? 2 : 4;
-  return rows <= 16 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
-}
-
 struct Launch {
-  int nt, target;
+  int nt;                    // row tiles of 16 nt rows in rows_kernel; 8: block_kernel's 128
+  int target;
   int64_t units, joins, slots;
 };
 
@@ -697,12 +1081,13 @@ struct Launch {
 // with at most 2 `target` pieces together.
 static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int64_t batch, int64_t max_pages,
                         int64_t max_q, Launch *L) {
-  const int64_t G = q_heads / kv.heads;
-  L->nt = row_tiles_of(max_q * G, kv.D);
+  const int64_t G = q_heads / kv.heads, most_rows = max_q * G;
+  L->nt = most_rows <= 16 ? 1 : most_rows <= 32 && kv.D <= 128 ? 2 : 8;
   const int64_t RT = 16 * L->nt;
-  const int64_t by_seq = batch * ((max_q * G + RT - 1) / RT), by_rows = total_q * G / RT + batch;
+  const int64_t by_seq = batch * ((most_rows + RT - 1) / RT), by_rows = total_q * G / RT + batch;
   const int64_t tiles = by_seq < by_rows ? by_seq : by_rows;
-  L->target = kTargetWgs / kv.heads > 0 ? kTargetWgs / kv.heads : 1;
+  const int wgs = L->nt == 1 && kv.D <= 128 ? 1024 : 512;
+  L->target = wgs / kv.heads > 0 ? wgs / kv.heads : 1;
   const int64_t steps = ((max_pages << kv.log_p) + kStep - 1) / kStep;
   if (steps > 1) {
     L->joins = tiles < L->target ? tiles : L->target;
@@ -716,8 +1101,10 @@ static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int6
   return L->units * kv.heads <= 0x7FFFFFFF && L->joins * RT * kv.heads <= 0x7FFFFFFF && steps * tiles <= 0x3FFFFFFF;
 }
 
+// Partial sums, (m, l), and the list of what is joined.
 static size_t workspace_of(const KvView &kv, const Launch &L) {
-  return (size_t)(L.slots * kv.heads * 16 * L.nt) * (kv.D + 2) * 4;
+  if (L.joins == 0) return 0;
+  return (size_t)(L.slots * kv.heads * 16 * L.nt) * (kv.D + 2) * 4 + 16 * (size_t)(L.joins + 1);
 }
 
 static nvfp4_status check_sizes(const KvView &kv, int64_t total_q, int32_t q_heads, int64_t batch, int64_t max_pages,
@@ -732,26 +1119,20 @@ static nvfp4_status check_sizes(const KvView &kv, int64_t total_q, int32_t q_hea
 
 template <int DP, int NT, bool F16>
 static void launch(const AttnArgs &A, const Launch &L, hipStream_t s) {
-  hipLaunchKernelGGL((rows_kernel<DP, NT, F16>), dim3((unsigned)(L.units * A.kv.heads)), dim3(256), 0, s, A);
+  constexpr int RT = 16 * NT, ROWS = NT == 8 ? 1024 / DP : 1;
+  const dim3 grid((unsigned)(L.units * A.kv.heads));
+  if constexpr (NT == 8) hipLaunchKernelGGL((block_kernel<DP, F16>), grid, dim3(256), 0, s, A);
+  else hipLaunchKernelGGL((rows_kernel<DP, NT, F16>), grid, dim3(256), 0, s, A);
   if (L.joins)
-    hipLaunchKernelGGL((join_kernel<DP, 16 * NT, F16>), dim3((unsigned)(L.joins * A.kv.heads * 16 * NT)), dim3(256), 0, s,
+    hipLaunchKernelGGL((join_kernel<DP, RT, ROWS, F16>), dim3((unsigned)(L.joins * A.kv.heads * (RT / ROWS))), dim3(256), 0, s,
                        A);
 }
 
-template <bool F16>
-static void launch_any(const AttnArgs &A, const Launch &L, hipStream_t s) {
-  if (A.kv.D <= 64) {
-    if (L.nt == 1) launch<64, 1, F16>(A, L, s);
-    else if (L.nt == 2) launch<64, 2, F16>(A, L, s);
-    else launch<64, 4, F16>(A, L, s);
-  } else if (A.kv.D <= 128) {
-    if (L.nt == 1) launch<128, 1, F16>(A, L, s);
-    else if (L.nt == 2) launch<128, 2, F16>(A, L, s);
-    else launch<128, 4, F16>(A, L, s);
-  } else {
-    if (L.nt == 1) launch<256, 1, F16>(A, L, s);
-    else launch<256, 2, F16>(A, L, s);
-  }
+template <int DP>
+static void launch_dim(const AttnArgs &A, const Launch &L, bool f16, hipStream_t s) {
+  if (L.nt == 1) f16 ? launch<DP, 1, true>(A, L, s) : launch<DP, 1, false>(A, L, s);
+  else if (L.nt == 8) f16 ? launch<DP, 8, true>(A, L, s) : launch<DP, 8, false>(A, L, s);
+  else if constexpr (DP <= 128) f16 ? launch<DP, 2, true>(A, L, s) : launch<DP, 2, false>(A, L, s);
 }
 
 }  // namespace nvfp4
@@ -815,9 +1196,15 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache *cache, nvfp4_rows q, int d
   A.target = L.target;
   A.slots = (int32_t)L.slots;
   A.part_o = (float *)ws;
-  A.part_ml = A.part_o + (L.slots * A.kv.heads * 16 * L.nt) * A.kv.D;
-  if (dtype == NVFP4_F16) launch_any<true>(A, L, (hipStream_t)stream);
-  else launch_any<false>(A, L, (hipStream_t)stream);
+  const int64_t part_rows = L.slots * A.kv.heads * 16 * L.nt;
+  A.part_ml = A.part_o + part_rows * A.kv.D;
+  A.join_count = (int32_t *)(A.part_ml + 2 * part_rows);
+  A.joins_at = A.join_count + 4;
+  A.joins = (int32_t)L.joins;
+  const bool f16 = dtype == NVFP4_F16;
+  if (A.kv.D <= 64) launch_dim<64>(A, L, f16, (hipStream_t)stream);
+  else if (A.kv.D <= 128) launch_dim<128>(A, L, f16, (hipStream_t)stream);
+  else launch_dim<256>(A, L, f16, (hipStream_t)stream);
   NVFP4_LAUNCH_CHECK();
   return NVFP4_OK;
 }
