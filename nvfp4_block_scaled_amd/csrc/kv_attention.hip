@@ -259,22 +259,35 @@ __device__ __forceinline__ void load_half(const KvView &kv, const LaneOffsets &o
   t.vs[st] = *reinterpret_cast<const uint32_t *>(head + at + o.vs);
 }
 
-// Loads the 32 keys from `base` on; bit st of the result: half st lies in a page of the pool.
-template <int DP>
-__device__ __forceinline__ uint32_t load_tile(const KvView &kv, const LaneOffsets &o, const int32_t *row, int cols,
-                                              int64_t head_at, int base, Tile<DP> &t) {
-  uint32_t ok = 0;
+// Page ids of a tile's two halves. They come through the scalar cache (the table is constant while
+// a kernel runs): their waits are counted apart from those of the vector loads, so asking for the
+// next tile's page does not wait for the present tile's bytes.
+typedef const __attribute__((address_space(4))) int32_t *ConstInts;
+
+struct Ids {
+  int id[2];
+};
+
+__device__ __forceinline__ Ids load_ids(const KvView &kv, ConstInts row, int cols, int base) {
+  Ids r;
 #pragma unroll
   for (int st = 0; st < 2; st++) {
-    const int key = base + 16 * st;
-    const int col = key >> kv.log_p;
-    const int page = col < cols ? row[col] : -1;
-    const bool in = page >= 0 && page < kv.num_pages;
-    if (in) ok |= 1u << st;
-    const uint8_t *head = kv.pages + (int64_t)(in ? page : 0) * kv.page_stride + head_at;
-    load_half<DP>(kv, o, head, (uint32_t)key & (kv.P() - 1u), t, st);
+    const int col = (base + 16 * st) >> kv.log_p;
+    const int id = row[min(col, cols - 1)];
+    r.id[st] = col < cols && id < kv.num_pages ? id : -1;
   }
-  return ok;
+  return r;
+}
+
+// Loads the 32 keys from `base` on (the first page of the pool where there is none).
+template <int DP>
+__device__ __forceinline__ void load_tile(const KvView &kv, const LaneOffsets &o, const Ids &ids, int64_t head_at,
+                                          int base, Tile<DP> &t) {
+#pragma unroll
+  for (int st = 0; st < 2; st++) {
+    const uint8_t *head = kv.pages + (int64_t)max(ids.id[st], 0) * kv.page_stride + head_at;
+    load_half<DP>(kv, o, head, (uint32_t)(base + 16 * st) & (kv.P() - 1u), t, st);
+  }
 }
 
 // The eight codes of one dword with the scale pair {s, s} -> eight exact FP16 products.
@@ -327,7 +340,7 @@ __device__ __forceinline__ float query_scale(float top, float *up) {
 // are read once by one wave, 20 registers a tile at D = 128, the next tile's in flight while the
 // present one is computed.
 template <int DP, int NT, bool F16>
-__global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 4 : 2) void rows_kernel(const AttnArgs A) {
+__global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel(const AttnArgs A) {
   constexpr int RT = 16 * NT, KS = Tile<DP>::KS, NB = Tile<DP>::NB, VD = Tile<DP>::VD, NU = Tile<DP>::NU;
   constexpr int OS = DP + 4;                             // row stride of the join buffer
   __shared__ float join_o[kWaves * 16 * OS];
@@ -352,6 +365,20 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 4 : 2) void rows_kernel
   const int steps = (max(0, hi - base0) + kStep - 1) / kStep;
   const int step0 = (int)((int64_t)steps * unit.split / unit.splits);
   const int step1 = (int)((int64_t)steps * (unit.split + 1) / unit.splits);
+
+  const LaneOffsets off = lane_offsets<DP>(kv);
+  const ConstInts row = (ConstInts)(uintptr_t)(A.table + (int64_t)unit.b * A.table_stride);
+  const int cols = (int)(((int64_t)s.len + kv.P() - 1) >> kv.log_p);     // table entries that hold keys
+  const int64_t head_at = (int64_t)head * kv.head_bytes();
+  // this wave's tiles: wave, wave + 4, ... of the piece; the first is on its way while the queries load
+  const int first = base0 + step0 * kStep + wave * kTile, end = min(hi, base0 + step1 * kStep);
+  Tile<DP> ta, tb;
+  Ids ia = {{-1, -1}}, ib = {{-1, -1}};
+  if (first < end) {
+    ia = load_ids(kv, row, cols, first);
+    ib = load_ids(kv, row, cols, first + kStep);
+    load_tile<DP>(kv, off, ia, head_at, first, ta);
+  }
 
   // this lane's column of S^T in each row tile: its query row, scaled by a power of two
   half8_t q[NT][KS];
@@ -395,10 +422,6 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 4 : 2) void rows_kernel
 #pragma unroll
     for (int d = 0; d < VD; d++) acc[nt][d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const LaneOffsets off = lane_offsets<DP>(kv);
-  const int32_t *row = A.table + (int64_t)unit.b * A.table_stride;
-  const int cols = (int)(((int64_t)s.len + kv.P() - 1) >> kv.log_p);     // table entries that hold keys
-  const int64_t head_at = (int64_t)head * kv.head_bytes();
   // scales of lanes past the head's elements are forced to zero
   uint32_t k_keep = 0;
 #pragma unroll
@@ -406,8 +429,8 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 4 : 2) void rows_kernel
     if (g * NB + i < D / 16) k_keep |= 0xFFu << (8 * i);
   const uint32_t v_keep = m * VD < D ? 0xFFFFFFFFu : 0u;
 
-  auto compute = [&](const Tile<DP> &t, int base, uint32_t ok) {
-    const bool whole = ok == 3u && base >= all_lo && base + kTile <= all_hi;      // every row sees every key
+  auto compute = [&](const Tile<DP> &t, int base, const Ids &ids) {
+    const bool whole = (ids.id[0] | ids.id[1]) >= 0 && base >= all_lo && base + kTile <= all_hi;      // every row sees every key
     // scores
     f32x4_t st[NT][2];
 #pragma unroll
@@ -430,7 +453,7 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 4 : 2) void rows_kernel
     if (!whole) {
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        const bool in = (ok >> h) & 1u;
+        const bool in = ids.id[h] >= 0;
         const int key0 = base + 16 * h + 4 * g;
         uint32_t keep = 0;
 #pragma unroll
@@ -538,19 +561,17 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 4 : 2) void rows_kernel
     }
   };
 
-  // this wave's tiles: wave, wave + 4, ... of the piece
-  const int first = base0 + step0 * kStep + wave * kTile, end = min(hi, base0 + step1 * kStep);
-  if (first < end) {
-    Tile<DP> a, b;
-    uint32_t oka = load_tile<DP>(kv, off, row, cols, head_at, first, a), okb = 0;
-    for (int base = first; base < end; base += 2 * kStep) {
-      const bool more = base + kStep < end;
-      if (more) okb = load_tile<DP>(kv, off, row, cols, head_at, base + kStep, b);
-      compute(a, base, oka);
-      if (!more) break;
-      if (base + 2 * kStep < end) oka = load_tile<DP>(kv, off, row, cols, head_at, base + 2 * kStep, a);
-      compute(b, base + kStep, okb);
-    }
+  for (int base = first; base < end; base += 2 * kStep) {
+    const bool more = base + kStep < end;
+    if (more) load_tile<DP>(kv, off, ib, head_at, base + kStep, tb);
+    const Ids ic = load_ids(kv, row, cols, base + 2 * kStep);
+    compute(ta, base, ia);
+    if (!more) break;
+    ia = ic;
+    if (base + 2 * kStep < end) load_tile<DP>(kv, off, ia, head_at, base + 2 * kStep, ta);
+    const Ids id = load_ids(kv, row, cols, base + 3 * kStep);
+    compute(tb, base + kStep, ib);
+    ib = id;
   }
 
   // join the four waves, 16 rows at a time
@@ -1001,8 +1022,10 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs A) {
   const KvView &kv = A.kv;
   const int group = blockIdx.x % (RT / ROWS), rest = blockIdx.x / (RT / ROWS);
   const int head = rest % kv.heads, j = rest / kv.heads;
-  if (j >= *A.join_count) return;
+  // (read beside the count, not after it: past the count it is whatever was there, and not used)
+  const int count = *A.join_count;
   const int row0 = A.joins_at[4 * j], rows = A.joins_at[4 * j + 1], slot = A.joins_at[4 * j + 2], splits = A.joins_at[4 * j + 3];
+  if (j >= count) return;
   if (group * ROWS >= rows || slot + splits > A.slots) return;
   const int D = kv.D, G = A.group;
   const int sl = threadIdx.x / TH, d = (threadIdx.x % TH) * 4;
@@ -1086,7 +1109,7 @@ static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int6
   const int64_t RT = 16 * L->nt;
   const int64_t by_seq = batch * ((most_rows + RT - 1) / RT), by_rows = total_q * G / RT + batch;
   const int64_t tiles = by_seq < by_rows ? by_seq : by_rows;
-  const int wgs = L->nt == 1 && kv.D <= 128 ? 1024 : 512;
+  const int wgs = L->nt == 1 && kv.D <= 128 ? 768 : 512;
   L->target = wgs / kv.heads > 0 ? wgs / kv.heads : 1;
   const int64_t steps = ((max_pages << kv.log_p) + kStep - 1) / kStep;
   if (steps > 1) {
