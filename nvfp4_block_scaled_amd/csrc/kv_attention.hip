@@ -24,6 +24,8 @@
 // end (k_g into the softmax's factor, v_g into the last division).
 #include <math.h>
 
+#include <type_traits>
+
 #include "kv_common.hpp"
 
 namespace nvfp4 {
@@ -190,14 +192,16 @@ __device__ __forceinline__ Range keys_of(const AttnArgs &A, const Seq &s, int i)
 // 32 keys of one wave as they lie in the cache. Lane (g = lane / 16, m = lane % 16) holds, for
 // each half of 16 keys, key m's codes of elements [g * DP / 4, (g + 1) * DP / 4) with their
 // scales, and the codes of values m * VD .. m * VD + VD - 1 of keys 4 g .. 4 g + 3 with theirs.
-template <int DP>
+template <int DP, bool ODD>
 struct Tile {
   static constexpr int KS = DP / 32;                   // products of 32 along a key's elements
   static constexpr int NB = DP / 64;                   // scale blocks of a lane's key elements
   static constexpr int VD = DP / 16;                   // value elements of a lane
   static constexpr int NU = DP == 256 ? 2 : 1;         // octets of value elements that a lane loads
   uint32_t kw[2][KS];
-  uint32_t ks[2];
+  // as loaded: widening here would wait for the load
+  typename std::conditional<NB == 4 && !ODD, uint32_t, typename std::conditional<NB == 2 && !ODD, uint16_t, uint8_t>::type>::type
+      ks[2][ODD ? NB : 1];
   u32x4_t vw[2][NU];
   uint32_t vs[2];
 };
@@ -222,41 +226,60 @@ __device__ __forceinline__ LaneOffsets lane_offsets(const KvView &kv) {
   return o;
 }
 
-template <int N>
-__device__ __forceinline__ uint32_t load_bytes(const uint8_t *p) {
-  uint32_t r = 0;
-  if (N == 1) {
-    r = *p;
-  } else {
-    if (N == 2) {
-      uint16_t h;
-      __builtin_memcpy(&h, p, 2);
-      r = h;
-    } else {
-      __builtin_memcpy(&r, p, 4);
-    }
-  }
-  return r;
+// One head's part of a page as a buffer: a uniform base with 32-bit offsets per lane (no 64-bit
+// address registers), and reads past the part return zero.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+
+__device__ __forceinline__ Buffer head_buffer(const KvView &kv, int page, int64_t head_at) {
+  const uint8_t *p = kv.pages + (int64_t)page * kv.page_stride + head_at;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, kv.head_bytes(), 0x00027000);
 }
 
-template <int DP>
-__device__ __forceinline__ void load_half(const KvView &kv, const LaneOffsets &o, const uint8_t *head, uint32_t at,
-                                          Tile<DP> &t, int st) {
-  const uint8_t *codes = head + at * (uint32_t)(kv.D / 2);
+template <int N>
+__device__ __forceinline__ uint32_t load_bytes(const uint8_t *p) {
+  uint16_t h;
+  static_assert(N == 2, "a pair of scales");
+  __builtin_memcpy(&h, p, 2);
+  return h;
+}
+
+// ODD: the scales of a lane do not lie at a multiple of their size (D is no multiple of DP / 4).
+template <int DP, bool ODD>
+__device__ __forceinline__ void load_half(const KvView &kv, const LaneOffsets &o, Buffer head, uint32_t at, Tile<DP, ODD> &t,
+                                          int st) {
+  constexpr int NB = Tile<DP, ODD>::NB;
+  const uint32_t codes = at * (uint32_t)(kv.D / 2), ks = at * (uint32_t)(kv.D / 16);
 #pragma unroll
-  for (int i = 0; i < Tile<DP>::KS / 4; i++) {
-    const u32x4_t w = *reinterpret_cast<const u32x4_a4 *>(codes + o.k + 16 * i);
+  for (int i = 0; i < Tile<DP, ODD>::KS / 4; i++) {
+    const u32x4_t w = __builtin_amdgcn_raw_buffer_load_b128(head, o.k + 16 * i, codes, 0);
 #pragma unroll
     for (int j = 0; j < 4; j++) t.kw[st][4 * i + j] = w[j];
   }
-  if (Tile<DP>::KS == 2) {
-    const u32x2_t w = *reinterpret_cast<const u32x2_a4 *>(codes + o.k);
+  if (Tile<DP, ODD>::KS == 2) {
+    const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(head, o.k, codes, 0);
     t.kw[st][0] = w[0], t.kw[st][1] = w[1];
   }
-  t.ks[st] = load_bytes<Tile<DP>::NB>(head + at * (uint32_t)(kv.D / 16) + o.ks);
+  if constexpr (NB == 1 || ODD) {
 #pragma unroll
-  for (int u = 0; u < Tile<DP>::NU; u++) t.vw[st][u] = *reinterpret_cast<const u32x4_t *>(codes + o.v + 16 * u);
-  t.vs[st] = *reinterpret_cast<const uint32_t *>(head + at + o.vs);
+    for (int i = 0; i < NB; i++) t.ks[st][i] = __builtin_amdgcn_raw_buffer_load_b8(head, o.ks + i, ks, 0);
+  } else if constexpr (NB == 2) {
+    t.ks[st][0] = __builtin_amdgcn_raw_buffer_load_b16(head, o.ks, ks, 0);
+  } else {
+    t.ks[st][0] = __builtin_amdgcn_raw_buffer_load_b32(head, o.ks, ks, 0);
+  }
+#pragma unroll
+  for (int u = 0; u < Tile<DP, ODD>::NU; u++) t.vw[st][u] = __builtin_amdgcn_raw_buffer_load_b128(head, o.v + 16 * u, codes, 0);
+  t.vs[st] = __builtin_amdgcn_raw_buffer_load_b32(head, o.vs, at, 0);
+}
+
+// The scale bytes of a lane's key elements in a half, as one word.
+template <int DP, bool ODD>
+__device__ __forceinline__ uint32_t key_scales(const Tile<DP, ODD> &t, int st) {
+  uint32_t w = t.ks[st][0];
+  if (ODD)
+#pragma unroll
+    for (int i = 1; i < Tile<DP, ODD>::NB; i++) w |= (uint32_t)t.ks[st][i] << (8 * i);
+  return w;
 }
 
 // Page ids of a tile's two halves. They come through the scalar cache (the table is constant while
@@ -265,29 +288,32 @@ __device__ __forceinline__ void load_half(const KvView &kv, const LaneOffsets &o
 typedef const __attribute__((address_space(4))) int32_t *ConstInts;
 
 struct Ids {
-  int id[2];
+  int id[2];             // as in the table: looked at only when the tile is loaded
 };
 
 __device__ __forceinline__ Ids load_ids(const KvView &kv, ConstInts row, int cols, int base) {
   Ids r;
 #pragma unroll
-  for (int st = 0; st < 2; st++) {
-    const int col = (base + 16 * st) >> kv.log_p;
-    const int id = row[min(col, cols - 1)];
-    r.id[st] = col < cols && id < kv.num_pages ? id : -1;
-  }
+  for (int st = 0; st < 2; st++) r.id[st] = row[min((base + 16 * st) >> kv.log_p, cols - 1)];
   return r;
 }
 
-// Loads the 32 keys from `base` on (the first page of the pool where there is none).
-template <int DP>
-__device__ __forceinline__ void load_tile(const KvView &kv, const LaneOffsets &o, const Ids &ids, int64_t head_at,
-                                          int base, Tile<DP> &t) {
+// Loads the 32 keys from `base` on. Returns bit st: half st has keys and lies in a page of the pool
+// (where not, the bytes are those of the first page).
+template <int DP, bool ODD>
+__device__ __forceinline__ uint32_t load_tile(const KvView &kv, const LaneOffsets &o, const Ids &ids, int cols,
+                                              int64_t head_at, int base, Tile<DP, ODD> &t) {
+  uint32_t ok = 0;
 #pragma unroll
   for (int st = 0; st < 2; st++) {
-    const uint8_t *head = kv.pages + (int64_t)max(ids.id[st], 0) * kv.page_stride + head_at;
-    load_half<DP>(kv, o, head, (uint32_t)(base + 16 * st) & (kv.P() - 1u), t, st);
+    const int key = base + 16 * st;
+    // column < cols and 0 <= id < num_pages, by sign bits: it stays on the scalar unit
+    const int id = ids.id[st];
+    const uint32_t in = (uint32_t)(((key >> kv.log_p) - cols) & ~id & (id - kv.num_pages)) >> 31;
+    ok |= in << st;
+    load_half<DP, ODD>(kv, o, head_buffer(kv, (int)in * id, head_at), (uint32_t)key & (kv.P() - 1u), t, st);
   }
+  return ok;
 }
 
 // The eight codes of one dword with the scale pair {s, s} -> eight exact FP16 products.
@@ -339,9 +365,9 @@ __device__ __forceinline__ float query_scale(float top, float *up) {
 // nothing is shared on the way, so there is no barrier in the loop. A key's and a value's bytes
 // are read once by one wave, 20 registers a tile at D = 128, the next tile's in flight while the
 // present one is computed.
-template <int DP, int NT, bool F16>
+template <int DP, int NT, bool F16, bool ODD>
 __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel(const AttnArgs A) {
-  constexpr int RT = 16 * NT, KS = Tile<DP>::KS, NB = Tile<DP>::NB, VD = Tile<DP>::VD, NU = Tile<DP>::NU;
+  constexpr int RT = 16 * NT, KS = Tile<DP, ODD>::KS, NB = Tile<DP, ODD>::NB, VD = Tile<DP, ODD>::VD, NU = Tile<DP, ODD>::NU;
   constexpr int OS = DP + 4;                             // row stride of the join buffer
   __shared__ float join_o[kWaves * 16 * OS];
   __shared__ float join_ml[kWaves][16][2];
@@ -372,12 +398,13 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
   const int64_t head_at = (int64_t)head * kv.head_bytes();
   // this wave's tiles: wave, wave + 4, ... of the piece; the first is on its way while the queries load
   const int first = base0 + step0 * kStep + wave * kTile, end = min(hi, base0 + step1 * kStep);
-  Tile<DP> ta, tb;
-  Ids ia = {{-1, -1}}, ib = {{-1, -1}};
+  Tile<DP, ODD> ta, tb;
+  Ids ib = {{0, 0}};
+  uint32_t oka = 0;
   if (first < end) {
-    ia = load_ids(kv, row, cols, first);
+    const Ids ia = load_ids(kv, row, cols, first);
     ib = load_ids(kv, row, cols, first + kStep);
-    load_tile<DP>(kv, off, ia, head_at, first, ta);
+    oka = load_tile<DP, ODD>(kv, off, ia, cols, head_at, first, ta);
   }
 
   // this lane's column of S^T in each row tile: its query row, scaled by a power of two
@@ -429,15 +456,15 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
     if (g * NB + i < D / 16) k_keep |= 0xFFu << (8 * i);
   const uint32_t v_keep = m * VD < D ? 0xFFFFFFFFu : 0u;
 
-  auto compute = [&](const Tile<DP> &t, int base, const Ids &ids) {
-    const bool whole = (ids.id[0] | ids.id[1]) >= 0 && base >= all_lo && base + kTile <= all_hi;      // every row sees every key
+  auto compute = [&](const Tile<DP, ODD> &t, int base, uint32_t ok) {
+    const bool whole = ok == 3u && base >= all_lo && base + kTile <= all_hi;      // every row sees every key
     // scores
     f32x4_t st[NT][2];
 #pragma unroll
     for (int h = 0; h < 2; h++) {
 #pragma unroll
       for (int nt = 0; nt < NT; nt++) st[nt][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      const uint32_t ksb = t.ks[h] & k_keep;
+      const uint32_t ksb = key_scales<DP, ODD>(t, h) & k_keep;
 #pragma unroll
       for (int k = 0; k < KS; k++) {
         const half2_t two = e4m3x2_to_f16(k / 2 >= 2 ? ksb >> 16 : ksb);
@@ -453,7 +480,7 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
     if (!whole) {
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        const bool in = ids.id[h] >= 0;
+        const bool in = (ok >> h) & 1u;
         const int key0 = base + 16 * h + 4 * g;
         uint32_t keep = 0;
 #pragma unroll
@@ -563,15 +590,14 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
 
   for (int base = first; base < end; base += 2 * kStep) {
     const bool more = base + kStep < end;
-    if (more) load_tile<DP>(kv, off, ib, head_at, base + kStep, tb);
-    const Ids ic = load_ids(kv, row, cols, base + 2 * kStep);
-    compute(ta, base, ia);
+    uint32_t okb = 0;
+    if (more) okb = load_tile<DP, ODD>(kv, off, ib, cols, head_at, base + kStep, tb);
+    const Ids ia = load_ids(kv, row, cols, base + 2 * kStep);
+    compute(ta, base, oka);
     if (!more) break;
-    ia = ic;
-    if (base + 2 * kStep < end) load_tile<DP>(kv, off, ia, head_at, base + 2 * kStep, ta);
-    const Ids id = load_ids(kv, row, cols, base + 3 * kStep);
-    compute(tb, base + kStep, ib);
-    ib = id;
+    if (base + 2 * kStep < end) oka = load_tile<DP, ODD>(kv, off, ia, cols, head_at, base + 2 * kStep, ta);
+    ib = load_ids(kv, row, cols, base + 3 * kStep);
+    compute(tb, base + kStep, okb);
   }
 
   // join the four waves, 16 rows at a time
@@ -917,14 +943,12 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
       const float shift = kOffset - (ref == -INFINITY ? 0.0f : ref);
 #pragma unroll
       for (int t = 0; t < T16; t++) {
-        half8_t p, seen;
+        half8_t p;
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-          const float x = st[t >> 1][8 * (t & 1) + j];
-          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x, c, shift));
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(st[t >> 1][8 * (t & 1) + j], c, shift));
           sum += e;
           p[j] = (_Float16)e;
-          if (nan_now) seen[j] = x == -INFINITY ? (_Float16)0.0f : (_Float16)1.0f;
         }
 #pragma unroll
         for (int d = 0; d < DT; d++) {
@@ -934,14 +958,15 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
           acc[d] = mfma32(a, p, acc[d]);
         }
         if (nan_now) {
-          // A row that sees a NaN value gets NaN in that value's block, and no other row does: the
+            // A row that sees a NaN value gets NaN in that value's block, and no other row does: the
           // product of "is NaN" and "is seen" counts them. (All of a lane's elements lie in a block.)
           const uint8_t *page = page_at(ids, t);
           const uint32_t at = (uint32_t)(base + 16 * t + 4 * hi) & (kv.P() - 1u);
           const uint32_t blk = min((uint32_t)(m % B::OCTETS) / 2, blocks - 1);
-          half8_t bad;
+          half8_t bad, seen;
 #pragma unroll
           for (int j = 0; j < 8; j++) {
+            seen[j] = st[t >> 1][8 * (t & 1) + j] == -INFINITY ? (_Float16)0.0f : (_Float16)1.0f;
             const uint32_t vs = page[kv.v_scales() + (blk << kv.log_p) + at + 8 * (j >> 2) + (j & 3)];
             bad[j] = (vs & 0x7Fu) == 0x7Fu && (ok >> t) & 1u ? (_Float16)1.0f : (_Float16)0.0f;
           }
@@ -1109,7 +1134,7 @@ static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int6
   const int64_t RT = 16 * L->nt;
   const int64_t by_seq = batch * ((most_rows + RT - 1) / RT), by_rows = total_q * G / RT + batch;
   const int64_t tiles = by_seq < by_rows ? by_seq : by_rows;
-  const int wgs = L->nt == 1 && kv.D <= 128 ? 768 : 512;
+  const int wgs = 512;
   L->target = wgs / kv.heads > 0 ? wgs / kv.heads : 1;
   const int64_t steps = ((max_pages << kv.log_p) + kStep - 1) / kStep;
   if (steps > 1) {
@@ -1145,7 +1170,8 @@ static void launch(const AttnArgs &A, const Launch &L, hipStream_t s) {
   constexpr int RT = 16 * NT, ROWS = NT == 8 ? 1024 / DP : 1;
   const dim3 grid((unsigned)(L.units * A.kv.heads));
   if constexpr (NT == 8) hipLaunchKernelGGL((block_kernel<DP, F16>), grid, dim3(256), 0, s, A);
-  else hipLaunchKernelGGL((rows_kernel<DP, NT, F16>), grid, dim3(256), 0, s, A);
+  else if (A.kv.D % (DP / 4) != 0) hipLaunchKernelGGL((rows_kernel<DP, NT, F16, true>), grid, dim3(256), 0, s, A);
+  else hipLaunchKernelGGL((rows_kernel<DP, NT, F16, false>), grid, dim3(256), 0, s, A);
   if (L.joins)
     hipLaunchKernelGGL((join_kernel<DP, RT, ROWS, F16>), dim3((unsigned)(L.joins * A.kv.heads * (RT / ROWS))), dim3(256), 0, s,
                        A);
