@@ -481,20 +481,18 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
 #pragma unroll
       for (int h = 0; h < 2; h++) {
         const bool in = (ok >> h) & 1u;
-        const int key0 = base + 16 * h + 4 * g;
+        // register i holds key at + i: compared as i with what is left of it
+        const int at = base + 16 * h + 4 * g, v_from = lo - at, v_to = hi - at;
+        const int past = min(s.len, s.len - s.queries + A.max_q) - at;
         uint32_t keep = 0;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          const int key = key0 + i;
-          if (in && key >= lo && key < hi) keep |= 0xFFu << (8 * i);
+          if (in && i >= v_from && i < v_to) keep |= 0xFFu << (8 * i);
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
-            bool see = in && key >= klo[nt] && key < khi[nt];
-            if (A.mask && in && key >= khi[nt] && key < s.len) {
-              const int j = key - (s.len - s.queries);             // which new token: >= 0, as khi <= key
-              see = j < A.max_q && mrow[nt][j] != 0;
-            }
-            st[nt][h][i] = see ? st[nt][h][i] : -INFINITY;
+            bool see = i >= klo[nt] - at && i < khi[nt] - at;
+            if (A.mask && i >= khi[nt] - at && i < past) see = mrow[nt][at - (s.len - s.queries) + i] != 0;
+            st[nt][h][i] = see && in ? st[nt][h][i] : -INFINITY;
           }
         }
         // values that no row sees count as zero; NaN ones that only some rows see go another way
@@ -697,6 +695,19 @@ __device__ __forceinline__ f32x16_t mfma32(half8_t a, half8_t b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
+// Order of a straight stretch of N matrix steps that each take one LDS fragment: AHEAD fragments are
+// on their way before the first step, and each step is followed by the read of a later step's. Left
+// alone, the compiler reads one or two right before the step that waits for them.
+template <int N, int AHEAD>
+__device__ __forceinline__ void pace() {
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);              // LDS reads
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);                  // a matrix instruction
+    if (i < N - AHEAD) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+}
+
 // A thread's part of a tile as it lies in the cache: 32 elements of one key, eight of four values.
 struct Raw {
   u32x4_t kw, vw;
@@ -768,7 +779,7 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
   }
 
   // which part of a tile this thread dequantizes
-  const bool k_task = wave < B::K_WAVES, v_task = wave >= B::V_FIRST;
+  const bool k_task = B::K_WAVES == kWaves || wave < B::K_WAVES, v_task = B::V_FIRST == 0 || wave >= B::V_FIRST;
   const int kg = k_task ? wave / B::PARTS : 0, part = k_task ? wave % B::PARTS : 0;
   const int kd0 = hi * (DP / 2) + part * 32;             // first element of its key part
   const int vw = wave - B::V_FIRST;
@@ -813,10 +824,21 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
       t.vs = *reinterpret_cast<const uint32_t *>(p + at + vs_off);
     }
   };
-  // Dequantizes this thread's part into buffer `buf`; true if it met a NaN value that some rows may
-  // not see (its scale then counts as zero: see nan_rows).
-  auto store_tile = [&](const Raw &t, int base, int buf) {
-    bool nan = false;
+  // Clears the scales of values that no row sees and, in a tile that some rows see only in part, of
+  // NaN values (the rows that see those are mended by themselves); true if there was one.
+  auto clear_unseen = [&](Raw &t, int base) {
+    const int at = base + 4 * tg, from = lo - at, to = end - at;
+    uint32_t keep = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      if (i >= from && i < to) keep |= 0xFFu << (8 * i);
+    const uint32_t bad = nan_bytes(t.vs & keep & v_keep);
+    t.vs &= keep & ~spread(bad);
+    return v_task && bad != 0u;
+  };
+  auto edge = [&](int base) { return base < all_lo || base + KT > all_hi; };
+  // Dequantizes this thread's part of a tile into buffer `buf`.
+  auto store_tile = [&](const Raw &t, int buf) {
     if (k_task) {
       const half2_t sc = e4m3x2_to_f16(t.ks & k_keep);
 #pragma unroll
@@ -829,19 +851,7 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
       }
     }
     if (v_task) {
-      uint32_t vs = t.vs & v_keep;
-      if (base < all_lo || base + KT > all_hi) {
-        uint32_t keep = 0;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int key = base + 4 * tg + i;
-          if (key >= lo && key < end) keep |= 0xFFu << (8 * i);
-        }
-        vs &= keep;
-        const uint32_t bad = nan_bytes(vs);
-        vs &= ~spread(bad);
-        nan = bad != 0u;
-      }
+      const uint32_t vs = t.vs & v_keep;
       const half2_t s01 = e4m3x2_to_f16(vs), s23 = e4m3x2_to_f16(vs >> 16);
       const uint32_t e01 = even_pairs(t.vw[0], t.vw[1]), o01 = odd_pairs(t.vw[0], t.vw[1]);
       const uint32_t e23 = even_pairs(t.vw[2], t.vw[3]), o23 = odd_pairs(t.vw[2], t.vw[3]);
@@ -864,7 +874,6 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
       NVFP4_KV_PUT(7, pair_value<3>(o01, s01), pair_value<3>(o23, s23))
 #undef NVFP4_KV_PUT
     }
-    return nan;
   };
 
   float ref = -INFINITY, sum = 0.0f;
@@ -874,23 +883,69 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
 #pragma unroll
     for (int i = 0; i < 16; i++) acc[d][i] = 0.0f;
 
-  bool nan_now = false, nan_next = false;
-  int ids = 0, ids_next = 0;
+  // Which keys of a tile this lane's row sees, register by register of S^T: key 32 g + o (o a constant
+  // of the register, less this half wave's 4 hi) when from <= 32 g + o < to; new keys under a tree
+  // mask from `to` up to `past`.
+  auto seen = [&](int base, uint32_t ok, auto put) {
+    const int at = base + 4 * hi, from = mine.lo - at, to = mine.hi - at, past = min(s.len, s.len - s.queries + A.max_q) - at;
+    const uint8_t *mk = A.mask ? mrow + (at - (s.len - s.queries)) : nullptr;
+#pragma unroll
+    for (int g = 0; g < KG; g++)
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        const int o = 32 * g + 8 * (i >> 2) + (i & 3);
+        bool see = o >= from && o < to;
+        if (A.mask && o >= to && o < past) see = mk[o] != 0;
+        put(g, i, see && ((ok >> (2 * g + (i >> 3))) & 1u));
+      }
+  };
+  // A row that sees a NaN value gets NaN in that value's block, and no other row does: the product of
+  // "is NaN" and "is seen" counts them. (All of a lane's elements lie in one block.)
+  auto nan_rows = [&](int base, int ids, uint32_t ok) {
+    f32x16_t n;
+#pragma unroll
+    for (int i = 0; i < 16; i++) n[i] = 0.0f;
+    half8_t see[T16];
+    seen(base, ok, [&](int g, int i, bool is) { see[2 * g + (i >> 3)][i & 7] = is ? (_Float16)1.0f : (_Float16)0.0f; });
+#pragma unroll
+    for (int t = 0; t < T16; t++) {
+      const uint8_t *page = page_at(ids, t);
+      const uint32_t at = (uint32_t)(base + 16 * t + 4 * hi) & (kv.P() - 1u);
+      const uint32_t blk = min((uint32_t)(m % B::OCTETS) / 2, blocks - 1);
+      half8_t bad;
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const uint32_t vs = page[kv.v_scales() + (blk << kv.log_p) + at + 8 * (j >> 2) + (j & 3)];
+        bad[j] = (vs & 0x7Fu) == 0x7Fu && (ok >> t) & 1u ? (_Float16)1.0f : (_Float16)0.0f;
+      }
+      n = mfma32(bad, see[t], n);
+    }
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+      for (int i = 0; i < 16; i++) acc[d][i] = n[i] > 0.0f ? __builtin_nanf("") : acc[d][i];
+  };
+
+  // While tile t is multiplied, tile t + 1 is on its way into registers; it is dequantized into the
+  // other buffer before the one barrier of a tile.
+  bool nan_now = false;
+  int ids = 0, ids1 = 0;
   Raw raw = {};
   if (first < last) {
     ids = load_ids(first);
     load_raw(ids, first, raw);
-    ids_next = load_ids(first + KT);
-    nan_now = store_tile(raw, first, 0);
+    ids1 = load_ids(first + KT);
+    if (edge(first)) nan_now = clear_unseen(raw, first);
+    store_tile(raw, 0);
   }
   nan_now = __syncthreads_or(nan_now);
   int buf = 0;
   for (int base = first; base < last; base += KT, buf ^= 1) {
     const bool more = base + KT < last;
-    int ids_after = 0;
+    int ids2 = 0;
     if (more) {
-      load_raw(ids_next, base + KT, raw);
-      ids_after = load_ids(base + 2 * KT);
+      load_raw(ids1, base + KT, raw);
+      ids2 = load_ids(base + 2 * KT);
     }
     if (working && base < w_hi && base + KT > w_lo) {
       f32x16_t st[KG];
@@ -906,23 +961,10 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
           st[g] = mfma32(a, q[k], st[g]);
         }
       }
+      pace<KG * KS, 4>();
       const uint32_t ok = (uint32_t)__ballot(ids >= 0 && ids < kv.num_pages) & ((1u << T16) - 1u);
-      const bool whole = ok == (1u << T16) - 1u && base >= wb.lo && base + KT <= wa.hi;
-      if (!whole) {
-#pragma unroll
-        for (int g = 0; g < KG; g++)
-#pragma unroll
-          for (int i = 0; i < 16; i++) {
-            const int key = base + 32 * g + 8 * (i >> 2) + 4 * hi + (i & 3);
-            const bool in = (ok >> (2 * g + (i >> 3))) & 1u;
-            bool see = in && key >= mine.lo && key < mine.hi;
-            if (A.mask && in && key >= mine.hi && key < s.len) {
-              const int j = key - (s.len - s.queries);
-              see = j < A.max_q && mrow[j] != 0;
-            }
-            st[g][i] = see ? st[g][i] : -INFINITY;
-          }
-      }
+      if (ok != (1u << T16) - 1u || base < wb.lo || base + KT > wa.hi)
+        seen(base, ok, [&](int g, int i, bool is) { st[g][i] = is ? st[g][i] : -INFINITY; });
       float top = st[0][0];
 #pragma unroll
       for (int g = 0; g < KG; g++)
@@ -957,39 +999,20 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
           __builtin_memcpy(&a, &w, 16);
           acc[d] = mfma32(a, p, acc[d]);
         }
-        if (nan_now) {
-            // A row that sees a NaN value gets NaN in that value's block, and no other row does: the
-          // product of "is NaN" and "is seen" counts them. (All of a lane's elements lie in a block.)
-          const uint8_t *page = page_at(ids, t);
-          const uint32_t at = (uint32_t)(base + 16 * t + 4 * hi) & (kv.P() - 1u);
-          const uint32_t blk = min((uint32_t)(m % B::OCTETS) / 2, blocks - 1);
-          half8_t bad, seen;
-#pragma unroll
-          for (int j = 0; j < 8; j++) {
-            seen[j] = st[t >> 1][8 * (t & 1) + j] == -INFINITY ? (_Float16)0.0f : (_Float16)1.0f;
-            const uint32_t vs = page[kv.v_scales() + (blk << kv.log_p) + at + 8 * (j >> 2) + (j & 3)];
-            bad[j] = (vs & 0x7Fu) == 0x7Fu && (ok >> t) & 1u ? (_Float16)1.0f : (_Float16)0.0f;
-          }
-          f32x16_t n;
-#pragma unroll
-          for (int i = 0; i < 16; i++) n[i] = 0.0f;
-          n = mfma32(bad, seen, n);
-#pragma unroll
-          for (int d = 0; d < DT; d++)
-#pragma unroll
-            for (int i = 0; i < 16; i++) acc[d][i] = n[i] > 0.0f ? __builtin_nanf("") : acc[d][i];
-        }
       }
+      if (nan_now) nan_rows(base, ids, ok);
     }
-    if (more) nan_next = store_tile(raw, base + KT, buf ^ 1);
+    bool nan_next = false;
+    const bool next_edge = more && edge(base + KT);
+    if (next_edge) nan_next = clear_unseen(raw, base + KT);
+    if (more) store_tile(raw, buf ^ 1);
     // (only tiles that some rows see in part look at values one by one)
-    if (more && (base + KT < all_lo || base + 2 * KT > all_hi)) nan_now = __syncthreads_or(nan_next);
+    if (next_edge) nan_now = __syncthreads_or(nan_next);
     else {
       __syncthreads();
       nan_now = false;
     }
-    ids = ids_next;
-    ids_next = ids_after;
+    ids = ids1, ids1 = ids2;
   }
   if (!working) return;
 
