@@ -15,8 +15,8 @@ namespace nvfp4 {
 static constexpr int kScanThreads = 1024;
 static constexpr int kPerThread = 16;                       // counts that a thread of a scan holds
 static constexpr int kScanSpan = kScanThreads * kPerThread;
-static constexpr int kSegment = 4096;                       // counts of one workgroup of the compact scan
-static constexpr int kSegThreads = 256;
+static constexpr int kNearStarts = 4096;
+static constexpr int kSegment = kScanSpan;                  // counts of one workgroup of the compact scan
 
 // Exclusive prefix sum over the workgroup; *total gets the sum. red: one int per wave, plus one.
 __device__ __forceinline__ int block_scan(int v, int *red, int *total) {
@@ -40,9 +40,21 @@ __device__ __forceinline__ int block_scan(int v, int *red, int *total) {
   return before + x - v;
 }
 
-// A count that atomics of this launch may have changed: read past the CU's own cache.
-__device__ __forceinline__ int load_count(const int32_t *p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// Which of the kPerThread counts from `first` on are above zero (LIVE) or not, as bits; none past `end`.
+template <bool LIVE>
+__device__ __forceinline__ uint32_t count_bits(const int32_t *refs, int64_t first, int64_t end) {
+  uint32_t bits = 0;
+  if (first + kPerThread <= end) {
+    u32x4_t w[kPerThread / 4];
+#pragma unroll
+    for (int i = 0; i < kPerThread / 4; i++) w[i] = *reinterpret_cast<const u32x4_a4 *>(refs + first + 4 * i);
+#pragma unroll
+    for (int i = 0; i < kPerThread; i++) bits |= ((int)w[i >> 2][i & 3] > 0) == LIVE ? 1u << i : 0u;
+  } else {
+    for (int i = 0; i < kPerThread; i++)
+      if (first + i < end && (refs[first + i] > 0) == LIVE) bits |= 1u << i;
+  }
+  return bits;
 }
 
 // ---------------------------------------------------------------- copying
@@ -102,6 +114,7 @@ struct ForkArgs {
   int32_t log_p, batch, children;
   int64_t width, table_stride, child_stride;
   const int32_t *table, *lens, *parents;
+  const int32_t *refs_in;
   int32_t *child_table, *refs, *short_dev;
   int32_t *src, *dst;              // workspace: the page each child copies, and where to (-1: none, -2: not served)
 };
@@ -119,10 +132,7 @@ __device__ __forceinline__ int take_pages(const int32_t *refs, int num_pages, in
   int found = 0;
   for (int64_t base = 0; base < num_pages && found < need; base += kScanSpan) {
     const int64_t first = base + (int64_t)threadIdx.x * kPerThread;
-    uint32_t free_bits = 0;
-#pragma unroll
-    for (int i = 0; i < kPerThread; i++)
-      if (first + i < num_pages && load_count(refs + first + i) <= 0) free_bits |= 1u << i;
+    uint32_t free_bits = count_bits<false>(refs, first, num_pages);
     int total;
     int rank = found + block_scan(__popc(free_bits), red, &total);
     while (free_bits && rank < need) {
@@ -171,7 +181,9 @@ __global__ __launch_bounds__(kScanThreads) void fork_plan_kernel(const ForkArgs 
   __syncthreads();
   // pages by rank go to the second half of the dst array
   int32_t *page_of = A.dst + A.children;
-  const int found = take_pages(A.refs, A.pool.num_pages, need, red, [&](int rank, int page) { page_of[rank] = page; });
+  const int found = take_pages(A.refs_in, A.pool.num_pages, need, red, [&](int rank, int page) { page_of[rank] = page; });
+  if (A.refs != A.refs_in && A.pool.num_pages <= kScanSpan)      // (a larger pool's counts are copied beforehand)
+    for (int i = threadIdx.x; i < A.pool.num_pages; i += kScanThreads) A.refs[i] = A.refs_in[i];
   __syncthreads();
   for (int c = threadIdx.x; c < A.children; c += kScanThreads) {
     const int rank = A.dst[c];
@@ -220,36 +232,29 @@ struct ResizeArgs {
   int32_t num_pages, log_p, batch;
   int64_t width, table_stride, out_stride;
   const int32_t *table, *lens, *new_lens;
-  const int32_t *refs_in;
   int32_t *table_out, *refs, *short_dev;
   int32_t *starts;                 // workspace [batch + 1]: entries that sequences before b take
 };
 
-// The grid's first batch blocks write a row each: kept entries, -1 elsewhere. With the table
-// resized in place, dropped entries are still to be read: they are left for the plan kernel.
-__global__ __launch_bounds__(256) void resize_rows_kernel(const ResizeArgs A, int in_place) {
+// A workgroup per sequence: gives back what it drops and writes its row: kept entries, -1 elsewhere.
+__global__ __launch_bounds__(256) void resize_rows_kernel(const ResizeArgs A) {
   const int b = blockIdx.x;
-  if (b < A.batch) {
-    const int was = (clamp_len(A.lens[b], A.width, A.log_p) + (1 << A.log_p) - 1) >> A.log_p;
-    const int now = (clamp_len(A.new_lens[b], A.width, A.log_p) + (1 << A.log_p) - 1) >> A.log_p;
-    for (int64_t i = threadIdx.x; i < A.width; i += 256) {
-      const bool drop = i >= now && i < was, grow = i >= was && i < now;
-      if (in_place) {
-        if (grow) A.table_out[b * A.out_stride + i] = -1;
-      } else {
-        A.table_out[b * A.out_stride + i] = (drop || grow) ? -1 : A.table[b * A.table_stride + i];
-      }
-    }
-  } else if (A.refs_in != A.refs) {
-    const int blocks = gridDim.x - A.batch;
-    for (int64_t i = (int64_t)(b - A.batch) * 256 + threadIdx.x; i < A.num_pages; i += (int64_t)blocks * 256)
-      A.refs[i] = A.refs_in[i];
+  const int was = (clamp_len(A.lens[b], A.width, A.log_p) + (1 << A.log_p) - 1) >> A.log_p;
+  const int now = (clamp_len(A.new_lens[b], A.width, A.log_p) + (1 << A.log_p) - 1) >> A.log_p;
+  const bool in_place = A.table == A.table_out;
+  for (int64_t i = (in_place ? min(was, now) : 0) + threadIdx.x; i < (in_place ? max(was, now) : A.width); i += 256) {
+    const bool drop = i >= now && i < was, grow = i >= was && i < now;
+    const int e = grow ? -1 : A.table[b * A.table_stride + i];
+    if (drop && e >= 0 && e < A.num_pages) atomicAdd(A.refs + e, -1);
+    A.table_out[b * A.out_stride + i] = (drop || grow) ? -1 : e;
   }
 }
 
-// One workgroup: gives dropped pages back, then hands free pages out in order.
-__global__ __launch_bounds__(kScanThreads) void resize_plan_kernel(const ResizeArgs A, int in_place) {
+// One workgroup: hands free pages out, in the order of sequences and positions.
+__global__ __launch_bounds__(kScanThreads) void resize_plan_kernel(const ResizeArgs A) {
   __shared__ int red[kScanThreads / 64 + 1];
+  __shared__ int near[kNearStarts];                 // the sequences' starts, where they fit: they are searched
+  const bool fits = A.batch <= kNearStarts;
   int need = 0;
   for (int base = 0; base < A.batch; base += kScanThreads) {
     const int b = base + threadIdx.x;
@@ -261,30 +266,19 @@ __global__ __launch_bounds__(kScanThreads) void resize_plan_kernel(const ResizeA
     }
     int total;
     const int before = need + block_scan(grow, red, &total);
-    if (b < A.batch) A.starts[b] = before;
+    if (b < A.batch) (fits ? near : A.starts)[b] = before;
     need += total;
   }
-  // a wave per sequence gives back what it drops
-  for (int b = threadIdx.x >> 6; b < A.batch; b += kScanThreads / 64) {
-    const int was = (clamp_len(A.lens[b], A.width, A.log_p) + (1 << A.log_p) - 1) >> A.log_p;
-    const int now = (clamp_len(A.new_lens[b], A.width, A.log_p) + (1 << A.log_p) - 1) >> A.log_p;
-    for (int i = now + (threadIdx.x & 63); i < was; i += 64) {
-      const int e = A.table[b * A.table_stride + i];
-      if (e >= 0 && e < A.num_pages) atomicAdd(A.refs + e, -1);
-      if (in_place) A.table_out[b * A.out_stride + i] = -1;
-    }
-  }
-  __threadfence();
   __syncthreads();
   const int found = take_pages(A.refs, A.num_pages, need, red, [&](int rank, int page) {
     int lo = 0, hi = A.batch - 1;                 // the last sequence whose start is <= rank
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (A.starts[mid] <= rank) lo = mid;
+      if ((fits ? near[mid] : A.starts[mid]) <= rank) lo = mid;
       else hi = mid - 1;
     }
     const int was = (clamp_len(A.lens[lo], A.width, A.log_p) + (1 << A.log_p) - 1) >> A.log_p;
-    A.table_out[lo * A.out_stride + was + (rank - A.starts[lo])] = page;
+    A.table_out[lo * A.out_stride + was + (rank - (fits ? near[lo] : A.starts[lo]))] = page;
     A.refs[page] = 1;
   });
   if (threadIdx.x == 0) *A.short_dev = need - found;
@@ -302,49 +296,46 @@ struct CompactArgs {
   int32_t *holes, *movers, *rank;  // workspace [num_pages] each; counts[segments] holds how many move
 };
 
-__device__ __forceinline__ uint32_t live_bits(const int32_t *refs, int64_t first, int64_t end) {
-  uint32_t bits = 0;
-#pragma unroll
-  for (int i = 0; i < kSegment / kSegThreads; i++)
-    if (first + i < end && refs[first + i] > 0) bits |= 1u << i;
-  return bits;
-}
-
-__global__ __launch_bounds__(kSegThreads) void compact_count_kernel(const CompactArgs A) {
-  __shared__ int red[kSegThreads / 64 + 1];
-  const int64_t first = (int64_t)blockIdx.x * kSegment + threadIdx.x * (kSegment / kSegThreads);
+__global__ __launch_bounds__(kScanThreads) void compact_count_kernel(const CompactArgs A) {
+  __shared__ int red[kScanThreads / 64 + 1];
+  const int64_t first = (int64_t)blockIdx.x * kSegment + threadIdx.x * kPerThread;
   int total;
-  block_scan(__popc(live_bits(A.refs, first, A.pool.num_pages)), red, &total);
+  block_scan(__popc(count_bits<true>(A.refs, first, A.pool.num_pages)), red, &total);
   if (threadIdx.x == 0) A.counts[blockIdx.x] = total;
 }
 
 // With n live pages: live id >= n -> the list of movers, free id < n -> the list of holes, both in
 // ascending order, so that mover r goes to hole r. A live page's rank among the live ones is the
 // prefix sum of the counts; a mover's rank is that less the live pages below n.
-__global__ __launch_bounds__(kSegThreads) void compact_plan_kernel(const CompactArgs A) {
-  __shared__ int red[kSegThreads / 64 + 1];
-  int all = 0, before = 0;
-  for (int i = threadIdx.x; i < A.segments; i += kSegThreads) {
-    const int c = A.counts[i];
-    all += c;
-    before += i < (int)blockIdx.x ? c : 0;
+__global__ __launch_bounds__(kScanThreads) void compact_plan_kernel(const CompactArgs A) {
+  __shared__ int red[kScanThreads / 64 + 1];
+  const int64_t first = (int64_t)blockIdx.x * kSegment + threadIdx.x * kPerThread;
+  const uint32_t bits = count_bits<true>(A.refs, first, A.pool.num_pages);
+  int live, mine = 0, total;
+  int rank = block_scan(__popc(bits), red, &total);
+  if (A.segments == 1) {
+    live = total;
+  } else {
+    int all = 0, before = 0;
+    for (int i = threadIdx.x; i < A.segments; i += kScanThreads) {
+      const int c = A.counts[i];
+      all += c;
+      before += i < (int)blockIdx.x ? c : 0;
+    }
+    block_scan(all, red, &live);
+    block_scan(before, red, &mine);                  // live pages before this segment
+    rank += mine;
   }
-  int live, mine, total;
-  block_scan(all, red, &live);
-  block_scan(before, red, &mine);                    // live pages before this segment
   const int cut = live / kSegment;                   // live pages below `live`: whole segments, then part of one
   int below = 0;
-  for (int i = threadIdx.x; i < cut; i += kSegThreads) below += A.counts[i];
-  const int64_t part = (int64_t)cut * kSegment + threadIdx.x * (kSegment / kSegThreads);
-  below += __popc(live_bits(A.refs, part, live));
+  for (int i = threadIdx.x; i < cut; i += kScanThreads) below += A.counts[i];
+  const int64_t part = (int64_t)cut * kSegment + threadIdx.x * kPerThread;
+  below += __popc(count_bits<true>(A.refs, part, live));
   int staying;
   block_scan(below, red, &staying);
 
-  const int64_t first = (int64_t)blockIdx.x * kSegment + threadIdx.x * (kSegment / kSegThreads);
-  const uint32_t bits = live_bits(A.refs, first, A.pool.num_pages);
-  int rank = mine + block_scan(__popc(bits), red, &total);
 #pragma unroll
-  for (int i = 0; i < kSegment / kSegThreads; i++) {
+  for (int i = 0; i < kPerThread; i++) {
     const int64_t id = first + i;
     if (id >= A.pool.num_pages) break;
     const bool alive = (bits >> i) & 1u;
@@ -451,6 +442,16 @@ int copy_grid(const Pool &pool, int64_t pairs, int cus) {
   return (int)(items < most ? (items < 1 ? 1 : items) : most);
 }
 
+// Counts for an operation that changes them elsewhere than in place.
+nvfp4_status copy_counts(const int32_t *from, int32_t *to, int64_t n, hipStream_t s) {
+  if (from == to) return NVFP4_OK;
+  const int64_t blocks = (n + 255) / 256;
+  hipLaunchKernelGGL(copy_counts_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(256), 0, s, from, to,
+                     (int)n);
+  NVFP4_LAUNCH_CHECK();
+  return NVFP4_OK;
+}
+
 nvfp4_status ws_ok(void *ws, size_t have, size_t need) {
   if (!ws || have < need) return NVFP4_ERR_WORKSPACE;
   return aligned(ws, 16) ? NVFP4_OK : NVFP4_ERR_ALIGN;
@@ -508,14 +509,9 @@ nvfp4_status nvfp4_kv_fork(const nvfp4_kv_pool *pool, int32_t page_size, const i
   A.batch = (int32_t)batch, A.children = (int32_t)children;
   A.width = width, A.table_stride = table_stride, A.child_stride = child_stride;
   A.table = table, A.lens = lens, A.parents = parents;
-  A.child_table = child_table, A.refs = refs_out, A.short_dev = short_dev;
+  A.child_table = child_table, A.refs_in = refs, A.refs = refs_out, A.short_dev = short_dev;
   A.src = (int32_t *)ws, A.dst = A.src + children;
-  if (refs_out != refs) {
-    const int64_t blocks = (A.pool.num_pages + 255) / 256;
-    hipLaunchKernelGGL(copy_counts_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(256), 0, s, refs,
-                       refs_out, A.pool.num_pages);
-    NVFP4_LAUNCH_CHECK();
-  }
+  if (A.pool.num_pages > kScanSpan && (st = copy_counts(refs, refs_out, A.pool.num_pages, s)) != NVFP4_OK) return st;
   hipLaunchKernelGGL(fork_plan_kernel, dim3(1), dim3(kScanThreads), 0, s, A);
   NVFP4_LAUNCH_CHECK();
   if (children == 0) return NVFP4_OK;
@@ -545,15 +541,13 @@ nvfp4_status nvfp4_kv_resize(int64_t num_pages, int32_t page_size, const int32_t
   ResizeArgs A = {};
   A.num_pages = (int32_t)num_pages, A.log_p = __builtin_ctz((unsigned)page_size), A.batch = (int32_t)batch;
   A.width = width, A.table_stride = table_stride, A.out_stride = table_out_stride;
-  A.table = table, A.lens = lens, A.new_lens = new_lens, A.refs_in = refs;
+  A.table = table, A.lens = lens, A.new_lens = new_lens;
   A.table_out = table_out, A.refs = refs_out, A.short_dev = short_dev;
   A.starts = (int32_t *)ws;
-  const int in_place = table == table_out;
-  int64_t extra = refs == refs_out ? 0 : (num_pages + 1023) / 1024;
-  if (extra > 512) extra = 512;
-  hipLaunchKernelGGL(resize_rows_kernel, dim3((unsigned)(batch + extra)), dim3(256), 0, s, A, in_place);
+  if ((st = copy_counts(refs, refs_out, num_pages, s)) != NVFP4_OK) return st;
+  hipLaunchKernelGGL(resize_rows_kernel, dim3((unsigned)batch), dim3(256), 0, s, A);
   NVFP4_LAUNCH_CHECK();
-  hipLaunchKernelGGL(resize_plan_kernel, dim3(1), dim3(kScanThreads), 0, s, A, in_place);
+  hipLaunchKernelGGL(resize_plan_kernel, dim3(1), dim3(kScanThreads), 0, s, A);
   NVFP4_LAUNCH_CHECK();
   return NVFP4_OK;
 }
@@ -580,9 +574,11 @@ nvfp4_status nvfp4_kv_compact(const nvfp4_kv_pool *pool, const int32_t *table, i
   A.width = width, A.table_stride = table_stride, A.out_stride = table_out_stride;
   A.table = table, A.refs = refs, A.table_out = table_out, A.refs_out = refs_out, A.live_dev = live_dev;
   A.holes = (int32_t *)ws, A.movers = A.holes + np, A.rank = A.movers + np, A.counts = A.rank + np;
-  hipLaunchKernelGGL(compact_count_kernel, dim3(A.segments), dim3(kSegThreads), 0, s, A);
-  NVFP4_LAUNCH_CHECK();
-  hipLaunchKernelGGL(compact_plan_kernel, dim3(A.segments), dim3(kSegThreads), 0, s, A);
+  if (A.segments > 1) {               // (a single segment's workgroup counts for itself)
+    hipLaunchKernelGGL(compact_count_kernel, dim3(A.segments), dim3(kScanThreads), 0, s, A);
+    NVFP4_LAUNCH_CHECK();
+  }
+  hipLaunchKernelGGL(compact_plan_kernel, dim3(A.segments), dim3(kScanThreads), 0, s, A);
   NVFP4_LAUNCH_CHECK();
   const int copies = copy_grid(A.pool, np / 2 + 1, d.num_cus);
   const int64_t tb = (width * batch + 1023) / 1024, rb = ((int64_t)np + 1023) / 1024;
