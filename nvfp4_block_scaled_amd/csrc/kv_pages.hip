@@ -233,7 +233,8 @@ struct ResizeArgs {
   int64_t width, table_stride, out_stride;
   const int32_t *table, *lens, *new_lens;
   int32_t *table_out, *refs, *short_dev;
-  int32_t *starts;                 // workspace [batch + 1]: entries that sequences before b take
+  int32_t *starts;                 // workspace [batch]: entries that sequences before b take,
+  int32_t *taken;                  // and [num_pages]: the pages in the order in which they are taken
 };
 
 // A workgroup per sequence: gives back what it drops and writes its row: kept entries, -1 elsewhere.
@@ -270,7 +271,13 @@ __global__ __launch_bounds__(kScanThreads) void resize_plan_kernel(const ResizeA
     need += total;
   }
   __syncthreads();
+  // first which pages, by the threads that find them free; then whose they are, a thread per page
   const int found = take_pages(A.refs, A.num_pages, need, red, [&](int rank, int page) {
+    A.taken[rank] = page;
+    A.refs[page] = 1;
+  });
+  __syncthreads();
+  for (int rank = threadIdx.x; rank < found; rank += kScanThreads) {
     int lo = 0, hi = A.batch - 1;                 // the last sequence whose start is <= rank
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -278,9 +285,8 @@ __global__ __launch_bounds__(kScanThreads) void resize_plan_kernel(const ResizeA
       else hi = mid - 1;
     }
     const int was = (clamp_len(A.lens[lo], A.width, A.log_p) + (1 << A.log_p) - 1) >> A.log_p;
-    A.table_out[lo * A.out_stride + was + (rank - (fits ? near[lo] : A.starts[lo]))] = page;
-    A.refs[page] = 1;
-  });
+    A.table_out[lo * A.out_stride + was + (rank - (fits ? near[lo] : A.starts[lo]))] = A.taken[rank];
+  }
   if (threadIdx.x == 0) *A.short_dev = need - found;
 }
 
@@ -543,7 +549,7 @@ nvfp4_status nvfp4_kv_resize(int64_t num_pages, int32_t page_size, const int32_t
   A.width = width, A.table_stride = table_stride, A.out_stride = table_out_stride;
   A.table = table, A.lens = lens, A.new_lens = new_lens;
   A.table_out = table_out, A.refs = refs_out, A.short_dev = short_dev;
-  A.starts = (int32_t *)ws;
+  A.starts = (int32_t *)ws, A.taken = A.starts + batch;    // (batch + num_pages <= 3 max(batch, num_pages))
   if ((st = copy_counts(refs, refs_out, num_pages, s)) != NVFP4_OK) return st;
   hipLaunchKernelGGL(resize_rows_kernel, dim3((unsigned)batch), dim3(256), 0, s, A);
   NVFP4_LAUNCH_CHECK();
