@@ -109,13 +109,10 @@ struct Unit {
   Seq s;
 };
 
-// Finds unit `u`; false past the last. Every wave does it for itself, a lane per sequence, with no
-// exchange through memory: pieces are as long as the call's steps over the workgroups to fill, and
-// a prefix sum over the sequences' pieces says whose piece `u` is. The first workgroup of each
-// split row tile leaves what join_kernel has to know of it. REVERSE: of a sequence under the causal
-// mask, the last row tile comes first: it sees the most keys.
-template <int RT, bool REVERSE>
-__device__ __forceinline__ bool find_unit(const AttnArgs &A, int u, bool tell, Unit *out) {
+// The sequences' shares, a lane per sequence (the first 64 of them are kept), and the pieces' length:
+// as long as the call's steps over the workgroups to fill.
+template <int RT>
+__device__ __forceinline__ Seq first_shares(const AttnArgs &A, int *chunk) {
   const int lane = threadIdx.x & 63;
   const Seq none = {0, 0, 0, 0, 0};
   const Seq s0 = lane < A.batch ? sequence<RT>(A, lane) : none;
@@ -124,17 +121,27 @@ __device__ __forceinline__ bool find_unit(const AttnArgs &A, int u, bool tell, U
     const Seq s = base + lane < A.batch ? sequence<RT>(A, base + lane) : none;
     total += last_lane(wave_scan(s.row_tiles * s.steps));
   }
-  const int chunk = max(1, (total + A.target - 1) / A.target);
-  int units = 0, slots = 0, joins = 0;
-  bool found = false;
+  *chunk = max(1, (total + A.target - 1) / A.target);
+  return s0;
+}
+
+// Finds unit `u`; false past the last. Every wave does it for itself with no exchange through memory:
+// a prefix sum over the sequences' pieces says whose piece `u` is. REVERSE: of a sequence under the
+// causal mask, the last row tile comes first: it sees the most keys.
+template <int RT, bool REVERSE>
+__device__ __forceinline__ bool find_unit(const AttnArgs &A, int u, Unit *out) {
+  const int lane = threadIdx.x & 63;
+  const Seq none = {0, 0, 0, 0, 0};
+  int chunk;
+  const Seq s0 = first_shares<RT>(A, &chunk);
+  int units = 0, slots = 0;
   for (int base = 0; base < A.batch; base += 64) {
     const Seq s = base == 0 ? s0 : base + lane < A.batch ? sequence<RT>(A, base + lane) : none;
     const int n = max(1, (s.steps + chunk - 1) / chunk);
-    const int mine = s.row_tiles * n, part = n > 1 ? mine : 0, join = n > 1 ? s.row_tiles : 0;
-    const int to = units + wave_scan(mine), slot_to = slots + wave_scan(part), join_to = joins + wave_scan(join);
+    const int mine = s.row_tiles * n, part = n > 1 ? mine : 0;
+    const int to = units + wave_scan(mine), slot_to = slots + wave_scan(part);
     const uint64_t hit = __ballot(u < to);
-    if (hit && !found) {
-      found = true;
+    if (hit) {
       const int at = __builtin_ctzll(hit);
       const int first = __builtin_amdgcn_readlane(to - mine, at);
       out->b = base + at;
@@ -147,25 +154,41 @@ __device__ __forceinline__ bool find_unit(const AttnArgs &A, int u, bool tell, U
       out->s.first = __builtin_amdgcn_readlane(s.first, at);
       out->s.row_tiles = __builtin_amdgcn_readlane(s.row_tiles, at);
       out->s.steps = __builtin_amdgcn_readlane(s.steps, at);
-      const int tile = out->tile;
-      if (REVERSE && A.causal) out->tile = out->s.row_tiles - 1 - tile;
-      if (tell && out->splits > 1 && out->split == 0) {
-        const int j = __builtin_amdgcn_readlane(join_to - join, at) + tile;
-        if (j < A.joins && threadIdx.x == 0) {
-          const int rows = min(out->s.queries, A.max_q) * A.group - out->tile * RT;
-          A.joins_at[4 * j] = out->s.first * A.group + out->tile * RT;       // (query, head of the group) row
-          A.joins_at[4 * j + 1] = min(rows, RT);
-          A.joins_at[4 * j + 2] = out->slot;
-          A.joins_at[4 * j + 3] = out->splits;
-        }
-      }
-      if (!tell || u != 0) return true;
+      if (REVERSE && A.causal) out->tile = out->s.row_tiles - 1 - out->tile;
+      return true;
     }
-    units = last_lane(to), slots = last_lane(slot_to), joins = last_lane(join_to);
+    units = last_lane(to), slots = last_lane(slot_to);
   }
-  // how many row tiles are to be joined (the first workgroup of the grid)
-  if (tell && u == 0 && threadIdx.x == 0) *A.join_count = joins;
-  return found;
+  return false;
+}
+
+// What join_kernel has to know of the split row tiles: a workgroup of its own (the grid's first)
+// lists them, the same prefix sums again.
+template <int RT, bool REVERSE>
+__device__ __forceinline__ void list_joins(const AttnArgs &A) {
+  if (threadIdx.x >= 64) return;
+  const int lane = threadIdx.x;
+  const Seq none = {0, 0, 0, 0, 0};
+  int chunk;
+  const Seq s0 = first_shares<RT>(A, &chunk);
+  int slots = 0, joins = 0;
+  for (int base = 0; base < A.batch; base += 64) {
+    const Seq s = base == 0 ? s0 : base + lane < A.batch ? sequence<RT>(A, base + lane) : none;
+    const int n = max(1, (s.steps + chunk - 1) / chunk);
+    const int tiles = n > 1 ? s.row_tiles : 0;
+    const int slot_to = slots + wave_scan(tiles * n), join_to = joins + wave_scan(tiles);
+    const int rows = min(s.queries, A.max_q) * A.group;
+    for (int i = 0; i < tiles; i++) {
+      const int j = join_to - tiles + i, tile = REVERSE && A.causal ? tiles - 1 - i : i;
+      if (j >= A.joins) break;
+      A.joins_at[4 * j] = s.first * A.group + tile * RT;          // (query, head of the group) row
+      A.joins_at[4 * j + 1] = min(rows - tile * RT, RT);
+      A.joins_at[4 * j + 2] = slot_to - tiles * n + i * n;
+      A.joins_at[4 * j + 3] = n;
+    }
+    slots = last_lane(slot_to), joins = last_lane(join_to);
+  }
+  if (lane == 0) *A.join_count = min(joins, A.joins);
 }
 
 // The keys that query i of a sequence sees: [lo, hi) (under a tree mask, those before the new ones).
@@ -372,9 +395,14 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
   __shared__ float join_o[kWaves * 16 * OS];
   __shared__ float join_ml[kWaves][16][2];
   const KvView &kv = A.kv;
-  const int head = blockIdx.x % kv.heads, u = blockIdx.x / kv.heads;
+  int block = blockIdx.x;
+  if (A.joins > 0 && --block < 0) {
+    list_joins<RT, false>(A);
+    return;
+  }
+  const int head = block % kv.heads, u = block / kv.heads;
   Unit unit;
-  if (!find_unit<RT, false>(A, u, A.joins > 0 && head == 0, &unit)) return;
+  if (!find_unit<RT, false>(A, u, &unit)) return;
   const Seq &s = unit.s;
   // (only with sequences that overlap in q_start)
   if (unit.tile < 0 || unit.tile >= s.row_tiles || (unit.splits > 1 && unit.slot >= A.slots)) return;
@@ -721,9 +749,14 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
   __shared__ u32x4_t kbuf[2][KG * KS * 64];
   __shared__ u32x4_t vbuf[2][DT * T16 * 64];
   const KvView &kv = A.kv;
-  const int head = blockIdx.x % kv.heads, u = blockIdx.x / kv.heads;
+  int block = blockIdx.x;
+  if (A.joins > 0 && --block < 0) {
+    list_joins<RT, true>(A);
+    return;
+  }
+  const int head = block % kv.heads, u = block / kv.heads;
   Unit unit;
-  if (!find_unit<RT, true>(A, u, A.joins > 0 && head == 0, &unit)) return;
+  if (!find_unit<RT, true>(A, u, &unit)) return;
   const Seq &s = unit.s;
   if (unit.tile < 0 || unit.tile >= s.row_tiles || (unit.splits > 1 && unit.slot >= A.slots)) return;
   const int lane = threadIdx.x & 63, m = lane & 31, hi = lane >> 5;
@@ -1062,13 +1095,13 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
 // each) and are a slice; ROWS rows share a workgroup, and the slices of a row take its pieces in
 // turn, eight loads in flight, and are added in order: the result does not depend on timing.
 template <int DP, int RT, int ROWS, bool F16>
-__global__ __launch_bounds__(256) void join_kernel(const AttnArgs A) {
+__global__ __launch_bounds__(256) void join_kernel(const AttnArgs A, int groups) {
   constexpr int TH = DP / 4, SL = 256 / TH / ROWS;      // threads of a slice, slices of a row
   static_assert(SL >= 1, "too many rows");
   __shared__ f32x4_t sm_o[ROWS * SL * TH];
   __shared__ float sm_ml[ROWS * SL][2];
   const KvView &kv = A.kv;
-  const int group = blockIdx.x % (RT / ROWS), rest = blockIdx.x / (RT / ROWS);
+  const int group = blockIdx.x % groups, rest = blockIdx.x / groups;
   const int head = rest % kv.heads, j = rest / kv.heads;
   // (read beside the count, not after it: past the count it is whatever was there, and not used)
   const int count = *A.join_count;
@@ -1145,6 +1178,7 @@ struct Launch {
   int nt;                    // row tiles of 16 nt rows in rows_kernel; 8: block_kernel's 128
   int target;
   int64_t units, joins, slots;
+  int rows;                  // rows of a row tile that can be there, in whole workgroups of join_kernel
 };
 
 // Sizes of a call from what the host knows of it (the lengths are on the device): pieces per KV
@@ -1155,6 +1189,8 @@ static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int6
   const int64_t G = q_heads / kv.heads, most_rows = max_q * G;
   L->nt = most_rows <= 16 ? 1 : most_rows <= 32 && kv.D <= 128 ? 2 : 8;
   const int64_t RT = 16 * L->nt;
+  const int64_t in_join = L->nt == 8 ? 1024 / (kv.D <= 64 ? 64 : kv.D <= 128 ? 128 : 256) : 1;
+  L->rows = (int)(((most_rows < RT ? most_rows : RT) + in_join - 1) / in_join * in_join);
   const int64_t by_seq = batch * ((most_rows + RT - 1) / RT), by_rows = total_q * G / RT + batch;
   const int64_t tiles = by_seq < by_rows ? by_seq : by_rows;
   const int wgs = 512;
@@ -1169,7 +1205,7 @@ static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int6
     L->joins = L->slots = 0;
     L->units = tiles;
   }
-  return L->units * kv.heads <= 0x7FFFFFFF && L->joins * RT * kv.heads <= 0x7FFFFFFF && steps * tiles <= 0x3FFFFFFF;
+  return L->units * kv.heads < 0x7FFFFFFF && L->joins * RT * kv.heads <= 0x7FFFFFFF && steps * tiles <= 0x3FFFFFFF;
 }
 
 // Partial sums, (m, l), and the list of what is joined.
@@ -1191,13 +1227,13 @@ static nvfp4_status check_sizes(const KvView &kv, int64_t total_q, int32_t q_hea
 template <int DP, int NT, bool F16>
 static void launch(const AttnArgs &A, const Launch &L, hipStream_t s) {
   constexpr int RT = 16 * NT, ROWS = NT == 8 ? 1024 / DP : 1;
-  const dim3 grid((unsigned)(L.units * A.kv.heads));
+  const dim3 grid((unsigned)(L.units * A.kv.heads + (L.joins ? 1 : 0)));
   if constexpr (NT == 8) hipLaunchKernelGGL((block_kernel<DP, F16>), grid, dim3(256), 0, s, A);
   else if (A.kv.D % (DP / 4) != 0) hipLaunchKernelGGL((rows_kernel<DP, NT, F16, true>), grid, dim3(256), 0, s, A);
   else hipLaunchKernelGGL((rows_kernel<DP, NT, F16, false>), grid, dim3(256), 0, s, A);
   if (L.joins)
-    hipLaunchKernelGGL((join_kernel<DP, RT, ROWS, F16>), dim3((unsigned)(L.joins * A.kv.heads * (RT / ROWS))), dim3(256), 0, s,
-                       A);
+    hipLaunchKernelGGL((join_kernel<DP, RT, ROWS, F16>), dim3((unsigned)(L.joins * A.kv.heads * (L.rows / ROWS))), dim3(256), 0,
+                       s, A, L.rows / ROWS);
 }
 
 template <int DP>

@@ -407,6 +407,30 @@ def test_other_stream_and_graph():
         assert torch.equal(out, eager[i]), i
 
 
+@pytest.mark.parametrize("hq,counts", [(8, [1, 1, 1]), (8, [20, 1, 3])])
+def test_workspace_needs_no_initialisation(hq, counts):
+    """Any bytes in the workspace, and one workspace for calls of several sizes in turn."""
+    r = synth.rng(19)
+    lens = np.array([9000, 40, 2500], np.int32)
+    pages, table, k_g, v_g = make_cache(r, lens, 32, 1, 128)
+    cache = nv.KVCache(dev(pages), 32, 1, 128, dev(k_g), dev(v_g))
+    tb, ln = dev(table), dev(lens)
+    T = sum(counts)
+    q = rounded(r.standard_normal((T, hq, 128)) * 0.1, "bf16")[0]
+    start = dev(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
+    ws = nv.nvfp4_kv_attention_workspace(T, hq, cache, 3, table.shape[1], max(counts))
+    assert ws is not None
+    want = nv.nvfp4_kv_attention(q, cache, tb, ln, start, max(counts))
+    for fill in (0, 0xFF, 0x7F, None, None):
+        if fill is None:
+            ws.copy_(torch.randint(0, 256, ws.shape, dtype=torch.uint8, device="cuda"))
+        else:
+            ws.fill_(fill)
+        for n in (ln, ln // 3, ln):
+            got = nv.nvfp4_kv_attention(q, cache, tb, n, start, max(counts), ws=ws)
+            assert n is not ln or torch.equal(got, want)
+
+
 # -------------------------------------------------------------------- pages
 
 def page_state(r, n_pages, batch, width, P, fill=0.6):
