@@ -109,19 +109,26 @@ struct Unit {
   Seq s;
 };
 
-// The sequences' shares, a lane per sequence (the first 64 of them are kept), and the pieces' length:
-// as long as the call's steps over the workgroups to fill.
+// The sequences' shares, a lane per sequence (the first 64 of them are kept), and how long pieces
+// are: the call's steps over the workgroups to fill. For block_kernel, whose workgroups are long, half
+// a workgroup for each row tile is set aside, so that all pieces run in one round, short last ones
+// included (256 queries on 32000 keys: 308 us without, 228 with; 64 on each of 16 sequences: 115
+// without, 111 with half, 154 with a whole one; rows_kernel's are short and many, and lose a tenth
+// by it); with more row tiles than workgroups only those several times longer than the average are
+// split.
 template <int RT>
 __device__ __forceinline__ Seq first_shares(const AttnArgs &A, int *chunk) {
   const int lane = threadIdx.x & 63;
   const Seq none = {0, 0, 0, 0, 0};
   const Seq s0 = lane < A.batch ? sequence<RT>(A, lane) : none;
-  int total = last_lane(wave_scan(s0.row_tiles * s0.steps));
+  int total = last_lane(wave_scan(s0.row_tiles * s0.steps)), tiles = last_lane(wave_scan(s0.row_tiles));
   for (int base = 64; base < A.batch; base += 64) {
     const Seq s = base + lane < A.batch ? sequence<RT>(A, base + lane) : none;
     total += last_lane(wave_scan(s.row_tiles * s.steps));
+    tiles += last_lane(wave_scan(s.row_tiles));
   }
-  *chunk = max(1, (total + A.target - 1) / A.target);
+  const int room = RT < kBlockRows ? A.target : max(A.target - tiles / 2, max(1, A.target / 4));
+  *chunk = max(1, (total + room - 1) / room);
   return s0;
 }
 
@@ -1082,7 +1089,12 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
       const int d = 8 * (mm % B::OCTETS) + DT * (mm / B::OCTETS);
       if (d >= D) continue;
 #pragma unroll
-      for (int j = 0; j < DT; j += 2) *reinterpret_cast<f32x2_t *>(A.part_o + at * D + d + j) = f32x2_t{acc[j][i], acc[j + 1][i]};
+      for (int j = 0; j < DT; j += DT >= 4 ? 4 : 2) {
+        if constexpr (DT >= 4)
+          *reinterpret_cast<f32x4_t *>(A.part_o + at * D + d + j) = f32x4_t{acc[j][i], acc[j + 1][i], acc[j + 2][i], acc[j + 3][i]};
+        else
+          *reinterpret_cast<f32x2_t *>(A.part_o + at * D + d + j) = f32x2_t{acc[j][i], acc[j + 1][i]};
+      }
     }
     if (hi == 0) A.part_ml[2 * at] = ref, A.part_ml[2 * at + 1] = sum;
   }
@@ -1178,22 +1190,22 @@ struct Launch {
   int nt;                    // row tiles of 16 nt rows in rows_kernel; 8: block_kernel's 128
   int target;
   int64_t units, joins, slots;
+  bool few;
   int rows;                  // rows of a row tile that can be there, in whole workgroups of join_kernel
 };
 
 // Sizes of a call from what the host knows of it (the lengths are on the device): pieces per KV
 // head are at most `target` + one for each row tile; row tiles that are split at most `target`,
-// with at most 2 `target` pieces together.
+// with at most 2 `target` pieces together (each has more steps than a piece, and the steps of all
+// are at most `target` pieces long).
 static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int64_t batch, int64_t max_pages,
                         int64_t max_q, Launch *L) {
   const int64_t G = q_heads / kv.heads, most_rows = max_q * G;
   L->nt = most_rows <= 16 ? 1 : most_rows <= 32 && kv.D <= 128 ? 2 : 8;
   const int64_t RT = 16 * L->nt;
-  const int64_t in_join = L->nt == 8 ? 1024 / (kv.D <= 64 ? 64 : kv.D <= 128 ? 128 : 256) : 1;
-  L->rows = (int)(((most_rows < RT ? most_rows : RT) + in_join - 1) / in_join * in_join);
   const int64_t by_seq = batch * ((most_rows + RT - 1) / RT), by_rows = total_q * G / RT + batch;
   const int64_t tiles = by_seq < by_rows ? by_seq : by_rows;
-  const int wgs = 512;
+  const int wgs = 512;       // two for each CU (64 ragged sequences, 262139 keys: 24.6 and 40 us; 256: 26.6 and 47; 1024: 28 and 46)
   L->target = wgs / kv.heads > 0 ? wgs / kv.heads : 1;
   const int64_t steps = ((max_pages << kv.log_p) + kStep - 1) / kStep;
   if (steps > 1) {
@@ -1205,6 +1217,13 @@ static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int6
     L->joins = L->slots = 0;
     L->units = tiles;
   }
+  // A workgroup of join_kernel takes eight rows (at D = 128) where there are many row tiles of few
+  // pieces, two with four times as many pieces in flight where there are few of many (one sequence of
+  // 8000 keys and 8 queries, 63 pieces: 20.8 us against 28; 32 drafted trees: 38.6 against 35).
+  const int DP = kv.D <= 64 ? 64 : kv.D <= 128 ? 128 : 256;
+  L->few = L->joins * kv.heads <= 32;
+  const int in_join = L->nt < 8 ? 1 : (L->few ? 256 : 1024) / DP;
+  L->rows = (int)(((most_rows < RT ? most_rows : RT) + in_join - 1) / in_join * in_join);
   return L->units * kv.heads < 0x7FFFFFFF && L->joins * RT * kv.heads <= 0x7FFFFFFF && steps * tiles <= 0x3FFFFFFF;
 }
 
@@ -1224,16 +1243,24 @@ static nvfp4_status check_sizes(const KvView &kv, int64_t total_q, int32_t q_hea
   return NVFP4_OK;
 }
 
+template <int DP, int NT, int ROWS, bool F16>
+static void launch_join(const AttnArgs &A, const Launch &L, hipStream_t s) {
+  hipLaunchKernelGGL((join_kernel<DP, 16 * NT, ROWS, F16>), dim3((unsigned)(L.joins * A.kv.heads * (L.rows / ROWS))),
+                     dim3(256), 0, s, A, L.rows / ROWS);
+}
+
 template <int DP, int NT, bool F16>
 static void launch(const AttnArgs &A, const Launch &L, hipStream_t s) {
-  constexpr int RT = 16 * NT, ROWS = NT == 8 ? 1024 / DP : 1;
   const dim3 grid((unsigned)(L.units * A.kv.heads + (L.joins ? 1 : 0)));
-  if constexpr (NT == 8) hipLaunchKernelGGL((block_kernel<DP, F16>), grid, dim3(256), 0, s, A);
-  else if (A.kv.D % (DP / 4) != 0) hipLaunchKernelGGL((rows_kernel<DP, NT, F16, true>), grid, dim3(256), 0, s, A);
-  else hipLaunchKernelGGL((rows_kernel<DP, NT, F16, false>), grid, dim3(256), 0, s, A);
-  if (L.joins)
-    hipLaunchKernelGGL((join_kernel<DP, RT, ROWS, F16>), dim3((unsigned)(L.joins * A.kv.heads * (L.rows / ROWS))), dim3(256), 0,
-                       s, A, L.rows / ROWS);
+  if constexpr (NT == 8) {
+    hipLaunchKernelGGL((block_kernel<DP, F16>), grid, dim3(256), 0, s, A);
+    if (L.joins && L.few) launch_join<DP, NT, 256 / DP, F16>(A, L, s);
+    else if (L.joins) launch_join<DP, NT, 1024 / DP, F16>(A, L, s);
+  } else {
+    if (A.kv.D % (DP / 4) != 0) hipLaunchKernelGGL((rows_kernel<DP, NT, F16, true>), grid, dim3(256), 0, s, A);
+    else hipLaunchKernelGGL((rows_kernel<DP, NT, F16, false>), grid, dim3(256), 0, s, A);
+    if (L.joins) launch_join<DP, NT, 1, F16>(A, L, s);
+  }
 }
 
 template <int DP>
