@@ -128,7 +128,7 @@ __device__ __forceinline__ Seq first_shares(const AttnArgs &A, int *chunk) {
     tiles += last_lane(wave_scan(s.row_tiles));
   }
   const int room = RT < kBlockRows ? A.target : max(A.target - tiles / 2, max(1, A.target / 4));
-  *chunk = max(1, (total + room - 1) / room);
+  *chunk = A.joins == 0 ? 1 << 30 : max(1, (total + room - 1) / room);
   return s0;
 }
 
@@ -1208,7 +1208,9 @@ static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int6
   const int wgs = 512;       // two for each CU (64 ragged sequences, 262139 keys: 24.6 and 40 us; 256: 26.6 and 47; 1024: 28 and 46)
   L->target = wgs / kv.heads > 0 ? wgs / kv.heads : 1;
   const int64_t steps = ((max_pages << kv.log_p) + kStep - 1) / kStep;
-  if (steps > 1) {
+  // Up to 1024 keys are not worth splitting for rows_kernel (731 keys, 4 KV heads: 9.5 us for one
+  // workgroup a head, 9.9 with pieces joined in a second launch, which costs the host 3 us more).
+  if (steps > (L->nt < 8 ? 8 : 1)) {
     L->joins = tiles < L->target ? tiles : L->target;
     const int64_t most = tiles * steps, slots = 2 * (int64_t)L->target;
     L->slots = most < slots ? most : slots;
