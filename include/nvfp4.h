@@ -419,13 +419,14 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int64_t *slots, in
  * (NaN scales too) does not reach the result. Query head h reads KV head
  * h / (q_heads / kv_heads).
  *  q       [total_q][q_heads][head_dim] of dtype BF16 or F16; out the same.
- *  table   device int32 [batch][>= max_pages], rows table_stride apart: page ids
- *          in order of position. Only the ceil(lens[b] / page_size) first are
+ *  table   device int32 [batch][>= max_pages], rows table_stride apart
+ *          (max_pages * page_size < 2^31 - 64 * page_size): page ids in order of
+ *          position. Only the ceil(lens[b] / page_size) first are
  *          read; an id outside the pool masks its keys.
  *  lens    device int32 [batch]: tokens in the cache, the new ones included
  *          (taken as 0 .. max_pages * page_size).
  *  q_start device int32 [batch + 1], ascending, or NULL: one query per sequence
- *          (total_q == batch).
+ *          (total_q == batch). Rows that no sequence has are not written.
  *  max_q   at least the longest sequence's n; queries of a sequence past it are
  *          not computed. The kernels are chosen by it.
  *  mask    device uint8 [total_q][max_q], rows mask_stride apart, or NULL.
@@ -475,7 +476,8 @@ nvfp4_status nvfp4_kv_copy_pages(const nvfp4_kv_pool *pool, const int32_t *src, 
  * finds no page, or has no such parent, or whose parent's length or partly
  * filled page is out of range, gets a row of -1 and is counted in short_dev
  * (device int32).
- *  child_table [children][width]; refs_out [num_pages]; refs_out may be refs. */
+ *  child_table [children][width], apart from table; refs_out [num_pages], which
+ *  may be refs. */
 nvfp4_status nvfp4_kv_fork(const nvfp4_kv_pool *pool, int32_t page_size, const int32_t *table, int64_t table_stride,
                            int64_t width, int64_t batch, const int32_t *lens, const int32_t *refs,
                            const int32_t *parents, int64_t children, int32_t *child_table, int64_t child_stride,

@@ -1241,7 +1241,8 @@ static nvfp4_status check_sizes(const KvView &kv, int64_t total_q, int32_t q_hea
   if (total_q < 0 || total_q > 0x3FFFFFFF / q_heads || batch < 0 || batch > (1 << 20) || max_q < 1 ||
       max_q > 0x7FFFFFFF)
     return NVFP4_ERR_SHAPE;
-  if (max_pages < 0 || max_pages > (0x7FFFFFFF >> kv.log_p) - 1) return NVFP4_ERR_SHAPE;
+  // (key numbers are 32-bit, and run some tiles past the last key)
+  if (max_pages < 0 || max_pages > (0x7FFFFFFF >> kv.log_p) - 64) return NVFP4_ERR_SHAPE;
   return NVFP4_OK;
 }
 

@@ -231,8 +231,11 @@ def nvfp4_kv_read(cache, slots, dtype=torch.bfloat16, k=None, v=None):
     T = _length(slots, "slots")
     slots_at = _flat(slots, "slots", dev, torch.int64, (T,))
     shape = (T, c.kv_heads, c.head_dim)
-    k = torch.empty(shape, dtype=dtype, device=slots.device) if k is None else k
-    v = torch.empty(shape, dtype=dtype, device=slots.device) if v is None else v
+    if k is None and v is None:
+        k, v = torch.empty((2,) + shape, dtype=dtype, device=slots.device).unbind(0)
+    else:
+        k = torch.empty(shape, dtype=dtype, device=slots.device) if k is None else k
+        v = torch.empty(shape, dtype=dtype, device=slots.device) if v is None else v
     k, ks = _rows(k, "k", dev, *shape, (dtype,), output=True)
     v, vs = _rows(v, "v", dev, *shape, (dtype,), output=True)
     _check(lib().nvfp4_kv_read(c._ref, slots_at, T, _DTYPES[dtype], ks, vs, _stream(dev)))

@@ -93,6 +93,7 @@ def test_attention_argument_checks():
     assert call(ts=99) == nv.ERR_SHAPE and call(mp=-1) == nv.ERR_SHAPE and call(max_q=0) == nv.ERR_SHAPE
     assert call(total=4) == nv.ERR_SHAPE                                    # one query per sequence
     assert call(total=1 << 40, qs=FAKE) == nv.ERR_SHAPE and call(mp=1 << 30) == nv.ERR_SHAPE
+    assert call(mp=(0x7FFFFFFF >> 4) - 63, ts=1 << 40) == nv.ERR_SHAPE
     for s in (0.0, -1.0, math.inf, math.nan):
         assert call(dict(scale=s)) == nv.ERR_VALUE
     assert call(dict(causal=2)) == nv.ERR_VALUE and call(dict(window=-1)) == nv.ERR_VALUE
