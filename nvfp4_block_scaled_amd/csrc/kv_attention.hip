@@ -1059,44 +1059,66 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
   sum += __shfl_xor(sum, 32, 64);
   const float vg = kv.v_g ? kv.v_g[head] : 1.0f;
   const bool final = unit.splits == 1;
-  if (row0 + 32 * wave + m > last_row) return;
-  // element d of column dt in register i: see store_tile for which it is
-  if (final) {
-    const int64_t t = s.first + qi;
-    const int h = head * G + gh;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / (sum * vg);
-    uint16_t *out = A.out + t * A.o_t + h * A.o_h;
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-      const int mm = 8 * (i >> 2) + 4 * hi + (i & 3);
-      const int d = 8 * (mm % B::OCTETS) + DT * (mm / B::OCTETS);
-      if (d >= D) continue;
-#pragma unroll
-      for (int j = 0; j < DT; j += 2) {
-        const uint32_t w = (uint32_t)pack1<F16>(acc[j][i] * inv) | ((uint32_t)pack1<F16>(acc[j + 1][i] * inv) << 16);
-        *reinterpret_cast<uint32_t *>(out + d + j) = w;
-      }
-    }
-    if (A.lse && hi == 0)
-      A.lse[t * (kv.heads * G) + h] = ref == -INFINITY && sum == 0.0f
-                                          ? -INFINITY
+  const int64_t slot_row = ((int64_t)unit.slot * kv.heads + head) * RT + 32 * wave;
+  const int h = head * G + gh;
+  if (hi == 0 && row0 + 32 * wave + m <= last_row) {
+    if (!final) {
+      A.part_ml[2 * (slot_row + m)] = ref, A.part_ml[2 * (slot_row + m) + 1] = sum;
+    } else if (A.lse) {
+      A.lse[(int64_t)(s.first + qi) * (kv.heads * G) + h] =
+          ref == -INFINITY && sum == 0.0f ? -INFINITY
                                           : (ref - kOffset + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
-  } else {
-    const int64_t at = ((int64_t)unit.slot * kv.heads + head) * RT + 32 * wave + m;
+    }
+  }
+  // A lane holds elements of one row: stored from there, 64 lanes write to 64 places. The wave's rows go
+  // through its quarter of the tiles' LDS (nobody reads tiles any more), 128 columns at a time, and leave
+  // in whole rows. Unit u of row m lies at u ^ m, so neither side conflicts.
+  constexpr int COLS = DP < 128 ? DP : 128, UNITS = COLS / 4, PHASES = DP / COLS;
+  static_assert(sizeof(kbuf) == 2 * 32 * UNITS * 16 && sizeof(vbuf) == sizeof(kbuf), "two waves' rows each");
+  f32x4_t *stage = reinterpret_cast<f32x4_t *>(wave < 2 ? &kbuf[0][0] : &vbuf[0][0]) + (wave & 1) * 32 * UNITS;
+  const float by = !final ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / (sum * vg);
+  const int64_t out_at = (int64_t)(s.first + qi) * A.o_t + (int64_t)h * A.o_h;
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
+  for (int ph = 0; ph < PHASES; ph++) {
+    // element d of column dt in register i: see store_tile for which it is
+#pragma unroll
+    for (int i = 16 / PHASES * ph; i < 16 / PHASES * (ph + 1); i++) {
       const int mm = 8 * (i >> 2) + 4 * hi + (i & 3);
-      const int d = 8 * (mm % B::OCTETS) + DT * (mm / B::OCTETS);
-      if (d >= D) continue;
+      const int unit4 = (8 * (mm % B::OCTETS) + DT * (mm / B::OCTETS) - COLS * ph) / 4;
+      if constexpr (DT >= 4) {
 #pragma unroll
-      for (int j = 0; j < DT; j += DT >= 4 ? 4 : 2) {
-        if constexpr (DT >= 4)
-          *reinterpret_cast<f32x4_t *>(A.part_o + at * D + d + j) = f32x4_t{acc[j][i], acc[j + 1][i], acc[j + 2][i], acc[j + 3][i]};
-        else
-          *reinterpret_cast<f32x2_t *>(A.part_o + at * D + d + j) = f32x2_t{acc[j][i], acc[j + 1][i]};
+        for (int j = 0; j < DT; j += 4)
+          stage[m * UNITS + ((unit4 + j / 4) ^ (m & (UNITS - 1)))] =
+              f32x4_t{acc[j][i] * by, acc[j + 1][i] * by, acc[j + 2][i] * by, acc[j + 3][i] * by};
+      } else {
+        float *at = reinterpret_cast<float *>(stage + m * UNITS + (unit4 ^ (m & (UNITS - 1))));
+        *reinterpret_cast<f32x2_t *>(at + (DT * (mm / B::OCTETS)) % 4) = f32x2_t{acc[0][i] * by, acc[1][i] * by};
       }
     }
-    if (hi == 0) A.part_ml[2 * at] = ref, A.part_ml[2 * at + 1] = sum;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (final) {
+      constexpr int PER = COLS / 8;                       // lanes of a row
+#pragma unroll
+      for (int n0 = 0; n0 < 32; n0 += 64 / PER) {
+        const int n = n0 + lane / PER, d = (lane % PER) * 8, at = d / 4;
+        const int64_t to = __shfl((long long)out_at, n, 64);
+        const f32x4_t y0 = stage[n * UNITS + (at ^ (n & (UNITS - 1)))], y1 = stage[n * UNITS + ((at + 1) ^ (n & (UNITS - 1)))];
+        const float x[8] = {y0[0], y0[1], y0[2], y0[3], y1[0], y1[1], y1[2], y1[3]};
+        if (row0 + 32 * wave + n <= last_row && COLS * ph + d < D)
+          *reinterpret_cast<u32x4_t *>(A.out + to + COLS * ph + d) = pack8<F16>(x);
+      }
+    } else {
+#pragma unroll
+      for (int n0 = 0; n0 < 32; n0 += 64 / UNITS) {
+        const int n = n0 + lane / UNITS, at = lane % UNITS;
+        const f32x4_t y = stage[n * UNITS + (at ^ (n & (UNITS - 1)))];
+        if (row0 + 32 * wave + n <= last_row && COLS * ph + 4 * at < D)
+          *reinterpret_cast<f32x4_t *>(A.part_o + (slot_row + n) * D + COLS * ph + 4 * at) = y;
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
