@@ -8,8 +8,8 @@
 //
 // The rows of one KV head are its queries times the query heads of its group:
 // row r is query r / G, head r % G of the group. Both products run on the
-// matrix cores transposed, S^T = K Q^T and O^T = V^T P^T, in 16 x 16 x 32 FP16
-// steps: a column of S^T and of O^T is one query row and stays in the same
+// matrix cores transposed, S^T = K Q^T and O^T = V^T P^T, in FP16 steps of
+// 16 x 16 x 32 (few rows) or 32 x 32 x 16 (many): a column of S^T and of O^T is one query row and stays in the same
 // lanes, so the softmax's scaling of O needs no exchange between lanes, and
 // P^T leaves the exponential already in the layout that the second product
 // takes (the order of its 32 keys is free as long as V's matches).
@@ -60,6 +60,17 @@ struct AttnArgs {
   int32_t joins;             // row tiles that the workspace has room for
 };
 
+// Asks for the arguments' cache lines before the first is needed: left alone, each line is a wait of
+// its own, some of them at the kernel's end (32 sequences of 3 to 8 queries: 34.9 -> 34.5 us).
+template <typename T>
+__device__ __forceinline__ void touch(T v) {
+  asm volatile("" ::"s"(v));
+}
+__device__ __forceinline__ void touch_args(const AttnArgs &A) {
+  touch(A.q); touch(A.out); touch(A.lse); touch(A.q_t); touch(A.o_t); touch(A.table); touch(A.lens); touch(A.mask);
+  touch(A.scale); touch(A.part_o); touch(A.joins_at); touch(A.kv.pages);
+}
+
 // ------------------------------------------------------------------- plan
 
 // One sequence's share of the work: rows in tiles of RT, keys in steps of kStep.
@@ -109,59 +120,89 @@ struct Unit {
   Seq s;
 };
 
-// The sequences' shares, a lane per sequence (the first 64 of them are kept), and how long pieces
-// are: the call's steps over the workgroups to fill. For block_kernel, whose workgroups are long, half
-// a workgroup for each row tile is set aside, so that all pieces run in one round, short last ones
-// included (256 queries on 32000 keys: 308 us without, 228 with; 64 on each of 16 sequences: 115
-// without, 111 with half, 154 with a whole one; rows_kernel's are short and many, and lose a tenth
-// by it); with more row tiles than workgroups only those several times longer than the average are
-// split.
-template <int RT>
-__device__ __forceinline__ Seq first_shares(const AttnArgs &A, int *chunk) {
-  const int lane = threadIdx.x & 63;
-  const Seq none = {0, 0, 0, 0, 0};
-  const Seq s0 = lane < A.batch ? sequence<RT>(A, lane) : none;
-  int total = last_lane(wave_scan(s0.row_tiles * s0.steps)), tiles = last_lane(wave_scan(s0.row_tiles));
-  for (int base = 64; base < A.batch; base += 64) {
-    const Seq s = base + lane < A.batch ? sequence<RT>(A, base + lane) : none;
-    total += last_lane(wave_scan(s.row_tiles * s.steps));
-    tiles += last_lane(wave_scan(s.row_tiles));
+// A lane's sequences from `base` on, PER each: one where a wave's lanes are enough, else four, whose
+// lengths are then on their way together (one token for each of 1024 sequences of 128 keys: 56 us, 80
+// with one to a lane, 63 with eight; 128 sequences: 22.6, 22.4, 23.6).
+template <int RT, int PER>
+__device__ __forceinline__ void shares(const AttnArgs &A, int base, Seq (&s)[PER]) {
+#pragma unroll
+  for (int i = 0; i < PER; i++) {
+    const int b = base + (threadIdx.x & 63) * PER + i;
+    s[i] = sequence<RT>(A, min(b, A.batch - 1));
+    if (b >= A.batch) s[i].row_tiles = s[i].steps = 0;
   }
-  const int room = RT < kBlockRows ? A.target : max(A.target - tiles / 2, max(1, A.target / 4));
-  *chunk = A.joins == 0 ? 1 << 30 : max(1, (total + room - 1) / room);
-  return s0;
 }
+
+// How many steps a piece has: the call's steps over the workgroups to fill. For block_kernel, whose
+// workgroups are long, half a workgroup for each row tile is set aside, so that all pieces run in one
+// round, short last ones included (256 queries on 32000 keys: 308 us without, 228 with; 64 on each of
+// 16 sequences: 115 without, 111 with half, 154 with a whole one; rows_kernel's are short and many, and
+// lose a tenth by it); with more row tiles than workgroups only those several times longer than the
+// average are split. s0: the first 64 PER sequences.
+template <int RT, int PER>
+__device__ __forceinline__ int piece_steps(const AttnArgs &A, Seq (&s0)[PER]) {
+  shares<RT, PER>(A, 0, s0);
+  if (A.joins == 0) return 1 << 30;
+  int total = 0, tiles = 0;
+#pragma unroll
+  for (int i = 0; i < PER; i++) total += s0[i].row_tiles * s0[i].steps, tiles += s0[i].row_tiles;
+  for (int base = 64 * PER; base < A.batch; base += 64 * PER) {
+    Seq s[PER];
+    shares<RT, PER>(A, base, s);
+#pragma unroll
+    for (int i = 0; i < PER; i++) total += s[i].row_tiles * s[i].steps, tiles += s[i].row_tiles;
+  }
+  total = last_lane(wave_scan(total)), tiles = last_lane(wave_scan(tiles));
+  const int room = RT < kBlockRows ? A.target : max(A.target - tiles / 2, max(1, A.target / 4));
+  return max(1, (total + room - 1) / room);
+}
+
+__device__ __forceinline__ int pieces_of(const Seq &s, int chunk) { return max(1, (s.steps + chunk - 1) / chunk); }
 
 // Finds unit `u`; false past the last. Every wave does it for itself with no exchange through memory:
 // a prefix sum over the sequences' pieces says whose piece `u` is. REVERSE: of a sequence under the
 // causal mask, the last row tile comes first: it sees the most keys.
-template <int RT, bool REVERSE>
-__device__ __forceinline__ bool find_unit(const AttnArgs &A, int u, Unit *out) {
-  const int lane = threadIdx.x & 63;
-  const Seq none = {0, 0, 0, 0, 0};
-  int chunk;
-  const Seq s0 = first_shares<RT>(A, &chunk);
+template <int RT, bool REVERSE, int PER>
+__device__ __forceinline__ bool find_unit_per(const AttnArgs &A, int u, Unit *out) {
+  Seq s[PER];
+  const int chunk = piece_steps<RT, PER>(A, s);
   int units = 0, slots = 0;
-  for (int base = 0; base < A.batch; base += 64) {
-    const Seq s = base == 0 ? s0 : base + lane < A.batch ? sequence<RT>(A, base + lane) : none;
-    const int n = max(1, (s.steps + chunk - 1) / chunk);
-    const int mine = s.row_tiles * n, part = n > 1 ? mine : 0;
+  for (int base = 0; base < A.batch; base += 64 * PER) {
+    if (base > 0) shares<RT, PER>(A, base, s);
+    int n[PER], mine = 0, part = 0;
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+      n[i] = pieces_of(s[i], chunk);
+      mine += s[i].row_tiles * n[i];
+      part += n[i] > 1 ? s[i].row_tiles * n[i] : 0;
+    }
     const int to = units + wave_scan(mine), slot_to = slots + wave_scan(part);
     const uint64_t hit = __ballot(u < to);
     if (hit) {
       const int at = __builtin_ctzll(hit);
-      const int first = __builtin_amdgcn_readlane(to - mine, at);
-      out->b = base + at;
-      out->splits = __builtin_amdgcn_readlane(n, at);
-      out->tile = (u - first) / out->splits;
-      out->split = (u - first) - out->tile * out->splits;
-      out->slot = __builtin_amdgcn_readlane(slot_to - part, at) + u - first;
-      out->s.len = __builtin_amdgcn_readlane(s.len, at);
-      out->s.queries = __builtin_amdgcn_readlane(s.queries, at);
-      out->s.first = __builtin_amdgcn_readlane(s.first, at);
-      out->s.row_tiles = __builtin_amdgcn_readlane(s.row_tiles, at);
-      out->s.steps = __builtin_amdgcn_readlane(s.steps, at);
-      if (REVERSE && A.causal) out->tile = out->s.row_tiles - 1 - out->tile;
+      int first = __builtin_amdgcn_readlane(to - mine, at), slot = __builtin_amdgcn_readlane(slot_to - part, at);
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < PER; i++) {
+        const int tiles = __builtin_amdgcn_readlane(s[i].row_tiles, at), splits = __builtin_amdgcn_readlane(n[i], at);
+        const int count = tiles * splits;
+        if (!found && (i == PER - 1 || u < first + count)) {
+          found = true;
+          out->b = base + at * PER + i;
+          out->splits = splits;
+          out->tile = (u - first) / splits;
+          out->split = (u - first) - out->tile * splits;
+          out->slot = slot + u - first;
+          out->s.len = __builtin_amdgcn_readlane(s[i].len, at);
+          out->s.queries = __builtin_amdgcn_readlane(s[i].queries, at);
+          out->s.first = __builtin_amdgcn_readlane(s[i].first, at);
+          out->s.row_tiles = tiles;
+          out->s.steps = __builtin_amdgcn_readlane(s[i].steps, at);
+          if (REVERSE && A.causal) out->tile = tiles - 1 - out->tile;
+        }
+        first += count;
+        if (splits > 1) slot += count;
+      }
       return true;
     }
     units = last_lane(to), slots = last_lane(slot_to);
@@ -169,19 +210,43 @@ __device__ __forceinline__ bool find_unit(const AttnArgs &A, int u, Unit *out) {
   return false;
 }
 
+template <int RT, bool REVERSE>
+__device__ __forceinline__ bool find_unit(const AttnArgs &A, int u, Unit *out) {
+  return A.batch <= 64 ? find_unit_per<RT, REVERSE, 1>(A, u, out) : find_unit_per<RT, REVERSE, 4>(A, u, out);
+}
+
+// Pieces of nearly the same length: piece i of `steps` begins at step begin(i).
+struct Pieces {
+  int each, longer;          // the first `longer` have one step more
+  __device__ __forceinline__ Pieces(int steps, int n) : each(steps / n), longer(steps - steps / n * n) {}
+  __device__ __forceinline__ int begin(int i) const { return each * i + min(i, longer); }
+};
+
+// Query and head of a row tile's rows: row k of the tile is query first + (rest + k) / G. Below 2^21 a
+// product with 1 / G tells (x + 1/2) / G from the next integer; a division is five times as long.
+struct RowQuery {
+  int first, rest, G;
+  float per;
+  __device__ __forceinline__ RowQuery(int row0, int g)
+      : first(row0 / g), rest(row0 - row0 / g * g), G(g), per(__builtin_amdgcn_rcpf((float)g)) {}
+  __device__ __forceinline__ int offset(int k) const { return (int)(((float)(rest + k) + 0.5f) * per); }
+  __device__ __forceinline__ int query(int k) const { return first + offset(k); }
+  __device__ __forceinline__ int head(int k) const { return rest + k - offset(k) * G; }
+};
+
 // What join_kernel has to know of the split row tiles: a workgroup of its own (the grid's first)
 // lists them, the same prefix sums again.
 template <int RT, bool REVERSE>
 __device__ __forceinline__ void list_joins(const AttnArgs &A) {
   if (threadIdx.x >= 64) return;
   const int lane = threadIdx.x;
-  const Seq none = {0, 0, 0, 0, 0};
-  int chunk;
-  const Seq s0 = first_shares<RT>(A, &chunk);
+  Seq one[1];
+  const int chunk = piece_steps<RT, 1>(A, one);
   int slots = 0, joins = 0;
   for (int base = 0; base < A.batch; base += 64) {
-    const Seq s = base == 0 ? s0 : base + lane < A.batch ? sequence<RT>(A, base + lane) : none;
-    const int n = max(1, (s.steps + chunk - 1) / chunk);
+    if (base > 0) shares<RT, 1>(A, base, one);
+    const Seq &s = one[0];
+    const int n = pieces_of(s, chunk);
     const int tiles = n > 1 ? s.row_tiles : 0;
     const int slot_to = slots + wave_scan(tiles * n), join_to = joins + wave_scan(tiles);
     const int rows = min(s.queries, A.max_q) * A.group;
@@ -395,6 +460,13 @@ __device__ __forceinline__ float query_scale(float top, float *up) {
 // nothing is shared on the way, so there is no barrier in the loop. A key's and a value's bytes
 // are read once by one wave, 20 registers a tile at D = 128, the next tile's in flight while the
 // present one is computed.
+//
+// Bound by the cache's bytes where there are many: one token on 262139 keys (151 MB, 4 heads of 128):
+// 32.8 us here and 6.3 in join_kernel, 4.6 TB/s of the 6.0 that a plain read reaches; one token for each
+// of 64 ragged sequences (54 MB): 19 + 4.9 us, of which about ten pass before the first tile is there and
+// after the last one. A single sequence of 731 keys (0.4 MB): 9.5 us, all latency; a launch that does
+// nothing but find no unit takes 5.6. 8 or 16 waves a workgroup, non-temporal loads and contiguous
+// shares of the waves measured slower or the same.
 template <int DP, int NT, bool F16, bool ODD>
 __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel(const AttnArgs A) {
   constexpr int RT = 16 * NT, KS = Tile<DP, ODD>::KS, NB = Tile<DP, ODD>::NB, VD = Tile<DP, ODD>::VD, NU = Tile<DP, ODD>::NU;
@@ -408,6 +480,8 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
     return;
   }
   const int head = block % kv.heads, u = block / kv.heads;
+  touch_args(A);
+  const float kg = kv.k_g ? kv.k_g[head] : 1.0f, vg = kv.v_g ? kv.v_g[head] : 1.0f;
   Unit unit;
   if (!find_unit<RT, false>(A, u, &unit)) return;
   const Seq &s = unit.s;
@@ -420,12 +494,13 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
   const int last_row = min(rows, row0 + RT) - 1;
 
   // keys of the tile's rows: all see [all_lo, all_hi), none sees outside [lo, hi)
-  const Range ra = keys_of(A, s, row0 / G), rb = keys_of(A, s, last_row / G);
+  const RowQuery rq(row0, G);
+  const Range ra = keys_of(A, s, rq.first), rb = keys_of(A, s, rq.query(last_row - row0));
   const int lo = ra.lo, hi = A.mask ? s.len : rb.hi, all_lo = rb.lo, all_hi = ra.hi;
   const int base0 = lo & ~(kTile - 1);
   const int steps = (max(0, hi - base0) + kStep - 1) / kStep;
-  const int step0 = (int)((int64_t)steps * unit.split / unit.splits);
-  const int step1 = (int)((int64_t)steps * (unit.split + 1) / unit.splits);
+  const Pieces pieces(steps, unit.splits);
+  const int step0 = pieces.begin(unit.split), step1 = pieces.begin(unit.split + 1);
 
   const LaneOffsets off = lane_offsets<DP>(kv);
   const ConstInts row = (ConstInts)(uintptr_t)(A.table + (int64_t)unit.b * A.table_stride);
@@ -447,11 +522,10 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
   float c[NT], ref[NT], sum[NT];
   int klo[NT], khi[NT];
   const uint8_t *mrow[NT];
-  const float kg = kv.k_g ? kv.k_g[head] : 1.0f;
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
-    const int r = min(row0 + 16 * nt + m, last_row);
-    const int i = r / G, gh = r - i * G;
+    const int r = min(16 * nt + m, last_row - row0);
+    const int i = rq.query(r), gh = rq.head(r);
     const Range kr = keys_of(A, s, i);
     klo[nt] = kr.lo, khi[nt] = kr.hi;
     mrow[nt] = A.mask ? A.mask + (int64_t)(s.first + i) * A.mask_stride : nullptr;
@@ -634,7 +708,6 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
   }
 
   // join the four waves, 16 rows at a time
-  const float vg = kv.v_g ? kv.v_g[head] : 1.0f;
   const bool final = unit.splits == 1;
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
@@ -678,7 +751,7 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
         for (int j = 0; j < 4; j++) x[j] += y0[j], x[j + 4] += y1[j];
       }
       if (final) {
-        const int i = r / G, gh = r - i * G;
+        const int i = rq.query(16 * nt + n), gh = rq.head(16 * nt + n);
         const int64_t t = s.first + i;
         const int h = head * G + gh;
         const float inv = l == 0.0f ? 0.0f : 1.0f / (l * vg);
@@ -713,6 +786,15 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
 // reads all of it. Two tiles are kept: while one is multiplied, the next one's codes are on their
 // way into registers, and they are dequantized into the other buffer before the one barrier of a
 // tile.
+//
+// Chunks of up to 2048 queries of 40 heads on 4 sequences of up to 8192 keys (508 GFLOP): 600 to 640 us,
+// 0.79 to 0.85 PFLOP/s (a plain 8192^3 product: 1.27). No unit is full: the matrix cores are busy a
+// third of the cycles, the vector units 55 % (350 instructions a wave and tile, of which a third is
+// the softmax and a quarter dequantizing), LDS 30 %; the two waves of a SIMD wait for data, barriers
+// and each other for the rest. Measured and not better: the next tile's dequantizing among the first
+// product's steps (620 against 605), fragments read ahead in the second product too (640 against 636),
+// codes two tiles ahead (600 against 606, for twice the code), tiles of 32 keys with three waves a SIMD
+// (834 against 600).
 template <int DP>
 struct Block {
   static constexpr int KT = DP == 256 ? 32 : 64;       // keys of a tile (LDS: 64 KiB at D >= 128)
@@ -762,6 +844,8 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
     return;
   }
   const int head = block % kv.heads, u = block / kv.heads;
+  touch_args(A);
+  const float gk = kv.k_g ? kv.k_g[head] : 1.0f, vg = kv.v_g ? kv.v_g[head] : 1.0f;
   Unit unit;
   if (!find_unit<RT, true>(A, u, &unit)) return;
   const Seq &s = unit.s;
@@ -770,21 +854,23 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int D = kv.D, G = A.group;
   const int rows = min(s.queries, A.max_q) * G, row0 = unit.tile * RT, last_row = min(rows, row0 + RT) - 1;
-  const Range ra = keys_of(A, s, row0 / G), rb = keys_of(A, s, last_row / G);
+  const RowQuery rq(row0, G);
+  const Range ra = keys_of(A, s, rq.first), rb = keys_of(A, s, rq.query(last_row - row0));
   const int lo = ra.lo, end = A.mask ? s.len : rb.hi, all_lo = rb.lo, all_hi = ra.hi;
   // this wave's rows (the last ones again where there are fewer)
-  const int w0 = min(row0 + 32 * wave, last_row), w1 = min(row0 + 32 * wave + 31, last_row);
+  const int w0 = min(32 * wave, last_row - row0), w1 = min(32 * wave + 31, last_row - row0);
   const bool working = row0 + 32 * wave <= last_row;
-  const Range wa = keys_of(A, s, w0 / G), wb = keys_of(A, s, w1 / G);
+  const Range wa = keys_of(A, s, rq.query(w0)), wb = keys_of(A, s, rq.query(w1));
   const int w_lo = wa.lo, w_hi = A.mask ? s.len : wb.hi;
   const int base0 = lo & ~(kStep - 1);
   const int steps = (max(0, end - base0) + kStep - 1) / kStep;
-  const int first = base0 + (int)((int64_t)steps * unit.split / unit.splits) * kStep;
-  const int last = min(end, base0 + (int)((int64_t)steps * (unit.split + 1) / unit.splits) * kStep);
+  const Pieces pieces(steps, unit.splits);
+  const int first = base0 + pieces.begin(unit.split) * kStep;
+  const int last = min(end, base0 + pieces.begin(unit.split + 1) * kStep);
 
   // this lane's column of S^T: its query row, scaled by a power of two
-  const int r = min(row0 + 32 * wave + m, last_row);
-  const int qi = r / G, gh = r - qi * G;
+  const int r = min(32 * wave + m, last_row - row0);
+  const int qi = rq.query(r), gh = rq.head(r);
   const Range mine = keys_of(A, s, qi);
   const uint8_t *mrow = A.mask ? A.mask + (int64_t)(s.first + qi) * A.mask_stride : nullptr;
   half8_t q[KS];
@@ -808,7 +894,7 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
     }
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     float up;
-    c = A.scale * 1.44269504088896f / (kv.k_g ? kv.k_g[head] : 1.0f) * query_scale(top, &up);
+    c = A.scale * 1.44269504088896f / gk * query_scale(top, &up);
 #pragma unroll
     for (int k = 0; k < KS; k++) {
       float x[8];
@@ -1057,7 +1143,6 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
   if (!working) return;
 
   sum += __shfl_xor(sum, 32, 64);
-  const float vg = kv.v_g ? kv.v_g[head] : 1.0f;
   const bool final = unit.splits == 1;
   const int64_t slot_row = ((int64_t)unit.slot * kv.heads + head) * RT + 32 * wave;
   const int h = head * G + gh;
@@ -1127,7 +1212,9 @@ __global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
 // Joins the pieces of a split row tile: with m_s, l_s, O_s of piece s and m = max m_s,
 // out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s. DP / 4 threads hold a row (four elements
 // each) and are a slice; ROWS rows share a workgroup, and the slices of a row take its pieces in
-// turn, eight loads in flight, and are added in order: the result does not depend on timing.
+// turn, eight loads in flight, and are added in order: the result does not depend on timing. 5 to 6 us,
+// the latency of two dependent loads and a launch; a workgroup that joins the pieces when it is the last
+// to finish saves the launch, but its device-scope fences cost 10 to 25 us.
 template <int DP, int RT, int ROWS, bool F16>
 __global__ __launch_bounds__(256) void join_kernel(const AttnArgs A, int groups) {
   constexpr int TH = DP / 4, SL = 256 / TH / ROWS;      // threads of a slice, slices of a row
@@ -1223,6 +1310,9 @@ struct Launch {
 static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int64_t batch, int64_t max_pages,
                         int64_t max_q, Launch *L) {
   const int64_t G = q_heads / kv.heads, most_rows = max_q * G;
+  // One token for each of 64 sequences (10 rows): 22.8 us with 16 rows a workgroup, 34.7 with 32. Three
+  // for each of 16 (30 rows): 21.1 with 32, 23.7 in block_kernel. Three to eight for each of 32 (80
+  // rows): 34 in block_kernel, 38 with 96 rows in rows_kernel.
   L->nt = most_rows <= 16 ? 1 : most_rows <= 32 && kv.D <= 128 ? 2 : 8;
   const int64_t RT = 16 * L->nt;
   const int64_t by_seq = batch * ((most_rows + RT - 1) / RT), by_rows = total_q * G / RT + batch;

@@ -283,6 +283,18 @@ def test_split_and_join(D, P, n):
     attend(23, [n, 77], [5, 4], 4, 2, D, P)
 
 
+@pytest.mark.parametrize("batch", [64, 65, 129, 300, 1030])
+def test_many_sequences(batch):
+    """More sequences than a wave has lanes: single tokens, several queries (some sequences have none), and a few long ones."""
+    r = synth.rng(batch)
+    lens = r.integers(0, 40, batch)
+    lens[[1, batch // 2, batch - 1]] = 1500, 0, 2100
+    attend(1000 + batch, lens, [1] * batch, 4, 2, 64, 16, q_start=False)
+    attend(2000 + batch, lens, r.integers(0, 4, batch), 10, 1, 64, 32, dtype="f16")
+    attend(3000 + batch, lens, r.integers(0, 3, batch), 36, 2, 64, 16)
+    attend(4000 + batch, np.minimum(lens, 60), r.integers(0, 2, batch), 4, 2, 128, 16)
+
+
 def test_query_shapes():
     """Strided and misaligned queries, a query of zeros, one with an infinity, and very small and large ones."""
     attend(31, [40, 77], [1, 1], 6, 2, 64, 16, q_start=False, pad=3)
