@@ -7,7 +7,9 @@
 // are those of any other implementation of these steps.
 //
 // Bound by memory: q, k and v come in once and q goes out once (the cache's 9/16
-// of a byte per element is small beside them). A thread owns eight pairs of one
+// of a byte per element is small beside them): 8192 tokens of 40 + 2 x 4 heads of
+// 128 (195 MB) take 41.7 us, 4.7 TB/s, the rate of a large copy; 64 tokens (1.5 MB)
+// 4.8 us and a read-back of them 4.5, a launch each. A thread owns eight pairs of one
 // token: their cosines and sines stay in registers over the heads of its group,
 // so the table is read once per group and not once per head. A turned key head
 // goes through LDS, because the pairs (j, j + rot/2) of one thread lie in two

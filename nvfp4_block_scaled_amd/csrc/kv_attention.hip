@@ -794,7 +794,9 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
 // and each other for the rest. Measured and not better: the next tile's dequantizing among the first
 // product's steps (620 against 605), fragments read ahead in the second product too (640 against 636),
 // codes two tiles ahead (600 against 606, for twice the code), tiles of 32 keys with three waves a SIMD
-// (834 against 600).
+// (834 against 600). At D > 128 a lane's sums and queries take 192 registers, and two waves a SIMD
+// would spill: one workgroup a CU then (chunks of 2048 queries on 8192 keys of 256 elements, 307 GFLOP:
+// 667 us, 888 with two that spill).
 template <int DP>
 struct Block {
   static constexpr int KT = DP == 256 ? 32 : 64;       // keys of a tile (LDS: 64 KiB at D >= 128)
@@ -832,7 +834,7 @@ struct Raw {
 };
 
 template <int DP, bool F16>
-__global__ __launch_bounds__(256, 2) void block_kernel(const AttnArgs A) {
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void block_kernel(const AttnArgs A) {
   using B = Block<DP>;
   constexpr int RT = kBlockRows, KT = B::KT, KG = B::KG, KS = B::KS, DT = B::DT, T16 = B::T16;
   __shared__ u32x4_t kbuf[2][KG * KS * 64];
@@ -1317,7 +1319,10 @@ static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int6
   const int64_t RT = 16 * L->nt;
   const int64_t by_seq = batch * ((most_rows + RT - 1) / RT), by_rows = total_q * G / RT + batch;
   const int64_t tiles = by_seq < by_rows ? by_seq : by_rows;
-  const int wgs = 512;       // two for each CU (64 ragged sequences, 262139 keys: 24.6 and 40 us; 256: 26.6 and 47; 1024: 28 and 46)
+  // Two workgroups for each CU (64 ragged sequences, 262139 keys: 24.6 and 40 us; one: 26.6 and 47;
+  // four: 28 and 46); one where only one is resident (256 queries on 32000 keys of 256 elements: 273 us
+  // against 301, 32 drafted trees 49 against 59).
+  const int wgs = L->nt == 8 && kv.D > 128 ? 256 : 512;
   L->target = wgs / kv.heads > 0 ? wgs / kv.heads : 1;
   const int64_t steps = ((max_pages << kv.log_p) + kStep - 1) / kStep;
   // Up to 1024 keys are not worth splitting for rows_kernel (731 keys, 4 KV heads: 9.5 us for one
