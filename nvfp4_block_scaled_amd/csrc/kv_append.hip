@@ -16,6 +16,7 @@
 // quantization blocks.
 #pragma clang fp contract(off)
 
+#include "e4m3.hpp"
 #include "kv_common.hpp"
 
 namespace nvfp4 {

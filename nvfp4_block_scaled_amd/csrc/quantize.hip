@@ -21,6 +21,7 @@
 #include <mutex>
 
 #include "common.hpp"
+#include "e4m3.hpp"
 
 namespace nvfp4 {
 
