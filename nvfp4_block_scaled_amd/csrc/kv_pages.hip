@@ -335,13 +335,17 @@ __global__ __launch_bounds__(kScanThreads) void compact_plan_kernel(const Compac
     block_scan(before, red, &mine);                  // live pages before this segment
     rank += mine;
   }
-  const int cut = live / kSegment;                   // live pages below `live`: whole segments, then part of one
-  int below = 0;
-  for (int i = threadIdx.x; i < cut; i += kScanThreads) below += A.counts[i];
-  const int64_t part = (int64_t)cut * kSegment + threadIdx.x * kPerThread;
-  below += __popc(count_bits<true>(A.refs, part, live));
-  int staying;
-  block_scan(below, red, &staying);
+  // Live pages below `live`: whole segments, then part of one. In a pool with no free page that is all of
+  // them, known without the counts (a full pool of one whole segment has none to read).
+  int staying = live;
+  if (live < A.pool.num_pages) {
+    const int cut = live / kSegment;
+    int below = 0;
+    for (int i = threadIdx.x; i < cut; i += kScanThreads) below += A.counts[i];
+    const int64_t part = (int64_t)cut * kSegment + threadIdx.x * kPerThread;
+    below += __popc(count_bits<true>(A.refs, part, live));
+    block_scan(below, red, &staying);
+  }
 
 #pragma unroll
   for (int i = 0; i < kPerThread; i++) {

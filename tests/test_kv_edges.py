@@ -1,0 +1,38 @@
+"""Edges of the key/value cache's operators: full pools, page ids without a page, very long windows, and arguments
+that only just do or do not fit."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_block_scaled_amd as nv
+import synth
+from oracle import kv
+from test_kv_cache import dev
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fill", [0, 0xFF])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n_pages", [16383, 16384, 16385, 32768])
+def test_compact_of_full_pools(n_pages, in_place, fill):
+    """No free page, or one, around the 16384 counts that one workgroup scans; any bytes in the workspace."""
+    r = synth.rng(n_pages)
+    pool = r.integers(0, 256, (2, n_pages, 16)).astype(np.uint8)
+    table = r.permutation(n_pages).astype(np.int32).reshape(1, -1)
+    ws = torch.empty(nv.lib().nvfp4_kv_pages_workspace_bytes(n_pages, 1), dtype=torch.uint8, device="cuda")
+    for free in (None, 0, n_pages // 2, n_pages - 1):
+        refs = r.integers(1, 5, n_pages).astype(np.int32)
+        if free is not None:
+            refs[free] = 0
+        pages, t, f = dev(pool), dev(table), dev(refs)
+        ws.fill_(fill)
+        got, new, live = nv.nvfp4_kv_compact(pages, t, f, out_table=t if in_place else None,
+                                             out_refs=f if in_place else None, ws=ws)
+        w_table, w_refs, w_live, moves = kv.compact(table, refs)
+        np.testing.assert_array_equal(got.cpu().numpy(), w_table)
+        np.testing.assert_array_equal(new.cpu().numpy(), w_refs)
+        assert int(live) == w_live
+        want = pool.copy()
+        for a, b in moves:
+            want[:, b] = want[:, a]
+        np.testing.assert_array_equal(pages.cpu().numpy(), want)
