@@ -827,10 +827,11 @@ __device__ __forceinline__ void pace() {
   }
 }
 
-// A thread's part of a tile as it lies in the cache: 32 elements of one key, eight of four values.
+// A thread's part of a tile as it lies in the cache: 32 elements of one key, eight of four values. vm: all
+// ones, or zero where the values' page id lies outside the pool (block_kernel's drop_scales).
 struct Raw {
   u32x4_t kw, vw;
-  uint32_t ks, vs;
+  uint32_t ks, vs, vm;
 };
 
 template <int DP, bool F16>
@@ -934,6 +935,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void block_kernel(const Att
     const int id = __builtin_amdgcn_readlane(ids, group);
     return kv.pages + (int64_t)(id >= 0 && id < kv.num_pages ? id : 0) * kv.page_stride + head_at;
   };
+  // Which of a tile's groups of 16 keys lie in a page of the pool, as bits.
+  constexpr uint32_t ALL = (1u << T16) - 1u;
+  auto inside = [&](int ids) { return (uint32_t)__ballot(ids >= 0 && ids < kv.num_pages) & ALL; };
   auto load_raw = [&](int ids, int base, Raw &t) {
     if (k_task) {
       const int key = base + 32 * kg + m;
@@ -950,7 +954,28 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void block_kernel(const Att
       const uint32_t at = (uint32_t)token & (kv.P() - 1u);
       t.vw = *reinterpret_cast<const u32x4_t *>(p + at * (uint32_t)(D / 2) + v_off);
       t.vs = *reinterpret_cast<const uint32_t *>(p + at + vs_off);
+      t.vm = 0xFFFFFFFFu;
+      if (DP == 128) {
+        const int id = __builtin_amdgcn_readlane(ids, vw);
+        t.vm = id >= 0 && id < kv.num_pages ? 0xFFFFFFFFu : 0u;
+      }
     }
+  };
+  // For an id outside the pool page_at gives the first page, whose owner may hold NaN there, and a zero
+  // probability does not cancel NaN: the values of such a group become zero. Where a wave's values lie in
+  // one page (D = 128) by a scalar mask on their scales, where they lie in two (64) by a select behind a
+  // branch, and at 256, where a wave has the fewest registers to spare, in LDS, by each wave that
+  // multiplies the tile, ahead of its own reads. Each costs the least of the three there: chunks of 64-,
+  // 128- and 256-wide heads took 401, 592 and 986 us with none of them, 395, 592 and 923 with these, 430,
+  // 597 and 1016 with masks, 418, 598 and 926 all in LDS.
+  auto drop_scales = [&](Raw &t, int ids) {
+    const uint32_t ok = inside(ids);
+    if (DP == 64 && ok != ALL) t.vs = (ok >> ((tg >> 2) & (T16 - 1))) & 1u ? t.vs : 0u;
+  };
+  auto drop_values = [&](int buf, uint32_t ok) {
+#pragma nounroll
+    for (int f = 0; f < DT * T16; f++)
+      if (!((ok >> (f % T16)) & 1u)) vbuf[buf][f * 64 + lane] = u32x4_t{0u, 0u, 0u, 0u};
   };
   // Clears the scales of values that no row sees and, in a tile that some rows see only in part, of
   // NaN values (the rows that see those are mended by themselves); true if there was one.
@@ -979,7 +1004,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void block_kernel(const Att
       }
     }
     if (v_task) {
-      const uint32_t vs = t.vs & v_keep;
+      const uint32_t vs = t.vs & v_keep & t.vm;
       const half2_t s01 = e4m3x2_to_f16(vs), s23 = e4m3x2_to_f16(vs >> 16);
       const uint32_t e01 = even_pairs(t.vw[0], t.vw[1]), o01 = odd_pairs(t.vw[0], t.vw[1]);
       const uint32_t e23 = even_pairs(t.vw[2], t.vw[3]), o23 = odd_pairs(t.vw[2], t.vw[3]);
@@ -1063,6 +1088,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void block_kernel(const Att
     ids = load_ids(first);
     load_raw(ids, first, raw);
     ids1 = load_ids(first + KT);
+    drop_scales(raw, ids);
     if (edge(first)) nan_now = clear_unseen(raw, first);
     store_tile(raw, 0);
   }
@@ -1090,9 +1116,11 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void block_kernel(const Att
         }
       }
       pace<KG * KS, 4>();
-      const uint32_t ok = (uint32_t)__ballot(ids >= 0 && ids < kv.num_pages) & ((1u << T16) - 1u);
-      if (ok != (1u << T16) - 1u || base < wb.lo || base + KT > wa.hi)
+      const uint32_t ok = inside(ids);
+      if (ok != ALL || base < wb.lo || base + KT > wa.hi) {
         seen(base, ok, [&](int g, int i, bool is) { st[g][i] = is ? st[g][i] : -INFINITY; });
+        if (DP == 256 && __builtin_expect(ok != ALL, 0)) drop_values(buf, ok);
+      }
       float top = st[0][0];
 #pragma unroll
       for (int g = 0; g < KG; g++)
@@ -1133,7 +1161,10 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void block_kernel(const Att
     bool nan_next = false;
     const bool next_edge = more && edge(base + KT);
     if (next_edge) nan_next = clear_unseen(raw, base + KT);
-    if (more) store_tile(raw, buf ^ 1);
+    if (more) {
+      drop_scales(raw, ids1);
+      store_tile(raw, buf ^ 1);
+    }
     // (only tiles that some rows see in part look at values one by one)
     if (next_edge) nan_now = __syncthreads_or(nan_next);
     else {

@@ -7,7 +7,7 @@ import torch
 import nvfp4_block_scaled_amd as nv
 import synth
 from oracle import kv
-from test_kv_cache import dev
+from test_kv_cache import attend, dev
 
 
 @pytest.mark.gpu
@@ -36,3 +36,22 @@ def test_compact_of_full_pools(n_pages, in_place, fill):
         for a, b in moves:
             want[:, b] = want[:, a]
         np.testing.assert_array_equal(pages.cpu().numpy(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,D,P,dtype", [(4, 2, 64, 16, "bf16"), (40, 2, 128, 64, "f16"), (4, 1, 256, 32, "bf16"),
+                                             (6, 2, 96, 16, "f16")])
+@pytest.mark.parametrize("cols", [[0], [1], [2, 3], [5, 7]])
+def test_nan_of_the_first_page_stays_out_of_ids_outside_the_pool(hq, hkv, D, P, dtype, cols):
+    """Ids without a page well inside a sequence; the page that is read in their place holds NaN in every value scale.
+    Few and many rows, in one piece and split."""
+    def edit(pages, table):
+        for col, bad in zip(cols, (-7, pages.shape[0])):
+            a = int(table[0, col])
+            pages[[0, a]] = pages[[a, 0]]                  # nobody else owns the first page
+            table[table == 0] = a
+            table[0, col] = bad
+        kv._sections(pages, P, hkv, D)[3][0] = 0x7F
+    for i, (lens, counts) in enumerate([([600], [1]), ([600], [40]), ([5000, 600], [40, 9])]):
+        attend(61 + i, lens, counts, hq, hkv, D, P, dtype, edit=edit)
+        attend(61 + i, lens, counts, hq, hkv, D, P, dtype, causal=False, edit=edit)
