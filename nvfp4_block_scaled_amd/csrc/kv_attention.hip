@@ -1431,9 +1431,9 @@ size_t nvfp4_kv_attention_workspace_bytes(const nvfp4_kv_cache *cache, int64_t t
                                           int64_t max_pages, int64_t max_q) {
   KvView kv;
   Launch L;
-  if (kv_view(cache, &kv) != NVFP4_OK || check_sizes(kv, total_q, q_heads, batch, max_pages, max_q) != NVFP4_OK ||
-      max_q > total_q + 1 || !plan_launch(kv, total_q, q_heads, batch, max_pages, max_q, &L))
-    return 0;
+  if (kv_view(cache, &kv) != NVFP4_OK || check_sizes(kv, total_q, q_heads, batch, max_pages, max_q) != NVFP4_OK) return 0;
+  if (max_q > total_q) max_q = total_q > 0 ? total_q : 1;         // as the call does
+  if (!plan_launch(kv, total_q, q_heads, batch, max_pages, max_q, &L)) return 0;
   return workspace_of(kv, L);
 }
 

@@ -1,5 +1,7 @@
 """Edges of the key/value cache's operators: full pools, page ids without a page, very long windows, and arguments
 that only just do or do not fit."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -55,3 +57,33 @@ def test_nan_of_the_first_page_stays_out_of_ids_outside_the_pool(hq, hkv, D, P, 
     for i, (lens, counts) in enumerate([([600], [1]), ([600], [40]), ([5000, 600], [40, 9])]):
         attend(61 + i, lens, counts, hq, hkv, D, P, dtype, edit=edit)
         attend(61 + i, lens, counts, hq, hkv, D, P, dtype, causal=False, edit=edit)
+
+
+FAKE, ODD = 0x10000, 0x10001            # never dereferenced: every call below is refused before a launch
+B = ctypes.byref
+
+
+def _descriptor(**kw):
+    a = dict(pages=FAKE, num_pages=8, page_stride=16 * 2 * 64 * 9 // 8, page_size=16, kv_heads=2, head_dim=64, reserved=0,
+             k_g=None, v_g=None)
+    a.update(kw)
+    return nv._Cache(*a.values())
+
+
+@pytest.mark.parametrize("total,heads", [(3, 4), (40, 4), (1, 2)])
+def test_workspace_query_takes_any_max_q_that_the_call_takes(total, heads):
+    """A caller may pass a fixed max_q: past total_q it asks for what the call asks for, and never for less."""
+    L, c, mask = nv.lib(), _descriptor(), nv._Mask(0.1, 1, 0, None, 0)
+    rows = nv._Rows(FAKE, 128, 64)
+    want = L.nvfp4_kv_attention_workspace_bytes(B(c), total, heads, 3, 100, total)
+    assert want > 0
+    for max_q in (total, total + 1, total + 2, total + 3, 1000, 0x7FFFFFFF):
+        need = L.nvfp4_kv_attention_workspace_bytes(B(c), total, heads, 3, 100, max_q)
+        assert need == want, max_q
+
+        def call(ws, n):
+            return L.nvfp4_kv_attention(B(c), rows, 1, total, heads, FAKE, 100, 100, FAKE, FAKE, 3, max_q, B(mask), rows, None,
+                                        ws, n, None)
+        assert call(FAKE, need - 1) == nv.ERR_WORKSPACE and call(ODD, need) == nv.ERR_ALIGN      # (enough, but misaligned)
+    assert L.nvfp4_kv_attention_workspace_bytes(B(c), total, heads, 3, 100, 0) == 0
+    assert L.nvfp4_kv_attention_workspace_bytes(B(c), total, heads, 3, 100, 1 << 31) == 0
