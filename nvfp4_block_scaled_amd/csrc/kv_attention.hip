@@ -1476,7 +1476,8 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache *cache, nvfp4_rows q, int d
   A.mask = mask->mask, A.mask_stride = mask->mask_stride;
   A.scale = mask->scale;
   A.causal = mask->causal;
-  A.window = mask->window > 0x3FFFFFFF ? 0 : (int32_t)mask->window;
+  // (a window as long as a sequence can be hides nothing)
+  A.window = mask->window >= max_pages << A.kv.log_p ? 0 : (int32_t)mask->window;
   A.batch = (int32_t)batch, A.max_q = (int32_t)max_q;
   A.group = q_heads / A.kv.heads;
   A.target = L.target;

@@ -1,6 +1,7 @@
 """Edges of the key/value cache's operators: full pools, page ids without a page, very long windows, and arguments
 that only just do or do not fit."""
 import ctypes
+import math
 
 import numpy as np
 import pytest
@@ -87,3 +88,35 @@ def test_workspace_query_takes_any_max_q_that_the_call_takes(total, heads):
         assert call(FAKE, need - 1) == nv.ERR_WORKSPACE and call(ODD, need) == nv.ERR_ALIGN      # (enough, but misaligned)
     assert L.nvfp4_kv_attention_workspace_bytes(B(c), total, heads, 3, 100, 0) == 0
     assert L.nvfp4_kv_attention_workspace_bytes(B(c), total, heads, 3, 100, 1 << 31) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [1, 40])
+def test_window_past_2_to_the_30(heads):
+    """A billion keys (one page, named over and over) behind a first page whose scores would outweigh them all: windows
+    that leave just that page out, and one that takes it in. Sums of equal terms: nothing to round but the output.
+    (1 is held as 6 times the E4M3 number next to 1 / 6, 0.171875.)"""
+    P, D, n = 256, 16, (1 << 30) + 1024
+    pages = torch.zeros((2, nv.nvfp4_kv_page_bytes(P, 1, D)), dtype=torch.uint8, device="cuda")
+    cache = nv.KVCache(pages, P, 1, D)
+    x = torch.full((P, 1, D), 6.0, dtype=torch.bfloat16, device="cuda")
+    at = torch.arange(P, device="cuda")
+    nv.nvfp4_kv_append(cache, x, x, at)
+    nv.nvfp4_kv_append(cache, x * 0, x / 6, at + P)
+    table = torch.ones((1, n // P), dtype=torch.int32, device="cuda")
+    table[0, 0] = 0
+    q = torch.full((1, heads, D), 4.0, dtype=torch.bfloat16, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    one = 6.0 * 0.171875
+    for window, value, lse in ((n - P, one, math.log(n - P)), (1 << 29, one, math.log(1 << 29)), (n, 6.0, 96 + math.log(P)),
+                               (1 << 40, 6.0, 96 + math.log(P))):
+        out, got = nv.nvfp4_kv_attention(q, cache, table, lens, window=window, return_lse=True)
+        assert bool((out == value).all()), window
+        assert bool(((got - lse).abs() <= 2.0 ** -20 * lse).all()), window
+
+
+@pytest.mark.gpu
+def test_window_as_long_as_the_table():
+    for window in (1, 95, 96, 97, 1 << 31, 1 << 62):
+        attend(71, [96, 50, 1], [1, 1, 1], 4, 2, 64, 16, q_start=False, window=window)
+        attend(72, [96, 50, 1], [30, 9, 1], 4, 2, 64, 16, window=window)
