@@ -487,8 +487,9 @@ nvfp4_status nvfp4_kv_fork(const nvfp4_kv_pool *pool, int32_t page_size, const i
  * (0: the sequence ends): first the entries past ceil(new / page_size) lose a
  * reference and become -1, then new entries take free pages in the order of
  * sequences and positions. Entries that find no page stay -1 and are counted in
- * short_dev. Lengths are taken as 0 .. width * page_size. A shared page that
- * becomes partly filled stays shared: fork before appending to it. */
+ * short_dev. Lengths are taken as 0 .. width * page_size; batch * width < 2^31.
+ * A shared page that becomes partly filled stays shared: fork before appending
+ * to it. */
 nvfp4_status nvfp4_kv_resize(int64_t num_pages, int32_t page_size, const int32_t *table, int64_t table_stride,
                              int64_t width, int64_t batch, const int32_t *lens, const int32_t *new_lens,
                              const int32_t *refs, int32_t *table_out, int64_t table_out_stride, int32_t *refs_out,

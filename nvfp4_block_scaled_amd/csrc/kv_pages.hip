@@ -546,6 +546,7 @@ nvfp4_status nvfp4_kv_resize(int64_t num_pages, int32_t page_size, const int32_t
   if (!ints_ok(lens) || !ints_ok(new_lens) || !ints_ok(refs) || !ints_ok(refs_out) || !ints_ok(short_dev))
     return NVFP4_ERR_ALIGN;
   if (table == table_out && batch > 1 && table_stride != table_out_stride) return NVFP4_ERR_SHAPE;
+  if (width > 0x7FFFFFFF / batch) return NVFP4_ERR_SHAPE;         // the plan adds up entries in 32 bits
   if ((st = ws_ok(ws, ws_bytes, nvfp4_kv_pages_workspace_bytes(num_pages, batch))) != NVFP4_OK) return st;
   DeviceInfo d;
   st = device_info(&d);

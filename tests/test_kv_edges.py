@@ -120,3 +120,15 @@ def test_window_as_long_as_the_table():
     for window in (1, 95, 96, 97, 1 << 31, 1 << 62):
         attend(71, [96, 50, 1], [1, 1, 1], 4, 2, 64, 16, q_start=False, window=window)
         attend(72, [96, 50, 1], [30, 9, 1], 4, 2, 64, 16, window=window)
+
+
+def test_resize_refuses_tables_whose_entries_pass_31_bits():
+    """The entries that sequences take are added up in 32 bits."""
+    def call(batch, width, ws):
+        need = nv.lib().nvfp4_kv_pages_workspace_bytes(8, batch)
+        return nv.lib().nvfp4_kv_resize(8, 1, FAKE, width, width, batch, FAKE, FAKE, FAKE, FAKE, width, FAKE, FAKE, ws, need,
+                                        None)
+    for batch, width in ((1 << 24, 128), (2, 1 << 30), (3, 0x7FFFFFFF // 3 + 1)):
+        assert call(batch, width, FAKE) == nv.ERR_SHAPE
+    for batch, width in ((1 << 24, 127), (1, 0x7FFFFFFF), (3, 0x7FFFFFFF // 3)):
+        assert call(batch, width, ODD) == nv.ERR_ALIGN             # taken, up to the misaligned workspace
