@@ -476,8 +476,8 @@ nvfp4_status nvfp4_kv_copy_pages(const nvfp4_kv_pool *pool, const int32_t *src, 
  * finds no page, or has no such parent, or whose parent's length or partly
  * filled page is out of range, gets a row of -1 and is counted in short_dev
  * (device int32).
- *  child_table [children][width], apart from table; refs_out [num_pages], which
- *  may be refs. */
+ *  child_table [children][width], apart from table (NVFP4_ERR_VALUE where they
+ *  share an entry); refs_out [num_pages], which may be refs. */
 nvfp4_status nvfp4_kv_fork(const nvfp4_kv_pool *pool, int32_t page_size, const int32_t *table, int64_t table_stride,
                            int64_t width, int64_t batch, const int32_t *lens, const int32_t *refs,
                            const int32_t *parents, int64_t children, int32_t *child_table, int64_t child_stride,

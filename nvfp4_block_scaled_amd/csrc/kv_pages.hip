@@ -445,6 +445,18 @@ nvfp4_status table_ok(const int32_t *table, int64_t stride, int64_t width, int64
   return aligned(table, 4) ? NVFP4_OK : NVFP4_ERR_ALIGN;
 }
 
+// Whether two tables with rows of `width` entries share none: one lies behind the other, or their rows
+// are different columns of one wider table.
+bool tables_apart(const int32_t *a, int64_t a_stride, int64_t a_rows, const int32_t *b, int64_t b_stride, int64_t b_rows,
+                  int64_t width) {
+  const __int128 a0 = (__int128)((uintptr_t)a / 4), b0 = (__int128)((uintptr_t)b / 4);
+  if (a0 + (__int128)(a_rows - 1) * a_stride + width <= b0 || b0 + (__int128)(b_rows - 1) * b_stride + width <= a0) return true;
+  if ((a_rows == 1 && b_rows == 1) || (a_rows > 1 && b_rows > 1 && a_stride != b_stride)) return false;
+  const int64_t stride = a_rows > 1 ? a_stride : b_stride;
+  const __int128 off = ((b0 - a0) % stride + stride) % stride;
+  return off >= width && off + width <= stride;
+}
+
 bool ints_ok(const void *p) { return aligned(p, 4); }
 
 // Blocks for copying `pairs` pages in all layers, eight workgroups for each CU at most.
@@ -514,6 +526,8 @@ nvfp4_status nvfp4_kv_fork(const nvfp4_kv_pool *pool, int32_t page_size, const i
       !ints_ok(child_table))
     return NVFP4_ERR_ALIGN;
   if ((st = ws_ok(ws, ws_bytes, nvfp4_kv_pages_workspace_bytes(pool->num_pages, children))) != NVFP4_OK) return st;
+  // a child's row written over a parent's that another child still reads
+  if (children > 0 && !tables_apart(table, table_stride, batch, child_table, child_stride, children, width)) return NVFP4_ERR_VALUE;
   DeviceInfo d;
   st = device_info(&d);
   if (st != NVFP4_OK) return st;

@@ -356,7 +356,8 @@ def nvfp4_kv_copy_pages(pages, src, dst):
 def nvfp4_kv_fork(pages, table, lens, refs, parents, page_size, out_table=None, out_refs=None, short=None, ws=None):
     """Forks sequences parents (int32 [children]): whole pages are shared, the partly filled one is copied
     to the lowest free page in all layers. Returns (child_table [children][width], refs, short int32 [1]:
-    children that could not be served, whose rows are -1). out_refs may be refs."""
+    children that could not be served, whose rows are -1). out_refs may be refs; out_table lies apart from
+    table (rows of the same table are refused, other columns of a wider one are not)."""
     dev = _device()
     n, pool = _pool(pages, dev)
     table_at, batch, width, stride = _table(table, "table", dev)

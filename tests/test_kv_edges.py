@@ -132,3 +132,49 @@ def test_resize_refuses_tables_whose_entries_pass_31_bits():
         assert call(batch, width, FAKE) == nv.ERR_SHAPE
     for batch, width in ((1 << 24, 127), (1, 0x7FFFFFFF), (3, 0x7FFFFFFF // 3)):
         assert call(batch, width, ODD) == nv.ERR_ALIGN             # taken, up to the misaligned workspace
+
+
+def test_fork_refuses_children_inside_the_table():
+    """Children's rows that share an entry with the table that is read (another child may still read it)."""
+    pool = nv._Pool(FAKE, 1, 0, 8, 64, 48)
+    need = nv.lib().nvfp4_kv_pages_workspace_bytes(8, 3)
+
+    def call(at, children, ts=10, cs=10, batch=4, width=4):
+        """table at FAKE, children `at` entries behind it."""
+        return nv.lib().nvfp4_kv_fork(B(pool), 16, FAKE, ts, width, batch, FAKE, FAKE, FAKE, children, FAKE + 4 * at, cs, FAKE, FAKE,
+                                      FAKE, need, None)
+    for at, children in ((0, 3), (0, 1), (1, 3), (3, 3), (7, 3), (9, 3), (20, 3), (30, 1), (33, 1), (-20, 3), (-23, 3)):
+        assert call(at, children) == nv.ERR_VALUE, (at, children)
+    assert call(3, 1, batch=1) == nv.ERR_VALUE and call(8, 3, cs=12) == nv.ERR_VALUE
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("at,children", [(34, 3), (4, 3), (6, 3), (5, 1), (24, 1), (-24, 3), (-26, 3), (-60, 3)])
+def test_fork_takes_children_beside_the_table(at, children):
+    """Before it, behind it, and in other columns of the same rows; table rows of 4 in 10."""
+    P, width = 16, 4
+    whole = torch.full((140,), -9, dtype=torch.int32, device="cuda")
+    table, child = whole[70:].as_strided((4, width), (10, 1)), whole[70 + at:].as_strided((children, width), (10, 1))
+    table.copy_(dev(np.array([[5, 0, 2, -1], [7, -1, -1, -1], [-1] * 4, [-1] * 4], np.int32)))
+    lens, refs = np.array([40, 16, 0, 0], np.int32), np.array([1, 0, 1, 0, 0, 1, 0, 1], np.int32)
+    parents = np.array([1, 0, 2], np.int32)[:children]
+    before = whole.cpu().numpy()
+    w_child, w_refs, w_short, _ = kv.fork(P, table.cpu().numpy(), lens, refs, parents)
+    pages = torch.zeros((8, 48), dtype=torch.uint8, device="cuda")
+    got, new, short = nv.nvfp4_kv_fork(pages, table, dev(lens), dev(refs), dev(parents), P, out_table=child)
+    assert got is child and int(short) == w_short == 0
+    np.testing.assert_array_equal(new.cpu().numpy(), w_refs)
+    for c in range(children):
+        before[70 + at + 10 * c:70 + at + 10 * c + width] = w_child[c]
+    np.testing.assert_array_equal(whole.cpu().numpy(), before)
+
+
+@pytest.mark.gpu
+def test_fork_refuses_rows_of_its_table():
+    table = torch.zeros((4, 3), dtype=torch.int32, device="cuda")
+    lens, refs = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.ones(8, dtype=torch.int32, device="cuda")
+    pages = torch.zeros((8, 48), dtype=torch.uint8, device="cuda")
+    for out in (table, table[2:], table[:2]):
+        parents = torch.zeros(out.shape[0], dtype=torch.int32, device="cuda")
+        with pytest.raises(ValueError):
+            nv.nvfp4_kv_fork(pages, table, lens, refs, parents, 16, out_table=out)
