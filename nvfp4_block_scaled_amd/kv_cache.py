@@ -124,7 +124,7 @@ def _rows(t, name, dev, tokens, heads, dim, dtypes, output=False):
         if output:
             raise ValueError(f"{name} needs a contiguous last dimension, a 16-byte aligned base and strides of "
                              "tokens and heads that are multiples of 8")
-        t = t.contiguous().clone()
+        t = t.clone(memory_format=torch.contiguous_format)
         ts, hs, at = heads * dim, dim, t.data_ptr()
     if output and not ((hs >= dim and ts >= heads * hs) or (ts >= dim and hs >= tokens * ts)
                        or (tokens <= 1 and hs >= dim) or (heads <= 1 and ts >= dim)):

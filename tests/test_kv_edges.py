@@ -178,3 +178,29 @@ def test_fork_refuses_rows_of_its_table():
         parents = torch.zeros(out.shape[0], dtype=torch.int32, device="cuda")
         with pytest.raises(ValueError):
             nv.nvfp4_kv_fork(pages, table, lens, refs, parents, 16, out_table=out)
+
+
+@pytest.mark.gpu
+def test_inputs_the_kernels_cannot_read_are_copied_once():
+    """A last dimension that is strided, rows at odd strides, a misaligned base: one new tensor of the same values."""
+    cache = nv.KVCache(torch.zeros((1, nv.nvfp4_kv_page_bytes(16, 2, 64)), dtype=torch.uint8, device="cuda"), 16, 2, 64)
+    slots, lens = torch.arange(3, device="cuda"), torch.full((3,), 3, dtype=torch.int32, device="cuda")
+    table = torch.zeros((3, 1), dtype=torch.int32, device="cuda")
+    good = torch.randn((3, 2, 64), device="cuda").to(torch.bfloat16)
+    strided, odd, shifted = (torch.empty(n, dtype=torch.bfloat16, device="cuda") for n in (768, 390, 385))
+    strided, odd, shifted = strided.view(3, 2, 128)[:, :, ::2], odd.view(3, 2, 65)[:, :, :64], shifted[1:].view(3, 2, 64)
+    out = torch.empty_like(good)
+    count = lambda: torch.cuda.memory_stats()["allocation.all.allocated"]     # noqa: E731
+
+    def made(x):
+        before = count()
+        nv.nvfp4_kv_append(cache, x, x, slots)
+        between = count()
+        nv.nvfp4_kv_attention(x, cache, table, lens, out=out)
+        return between - before, count() - between
+    assert made(good) == (0, 0)
+    want = out.clone()
+    for x in (strided, odd, shifted):
+        x.copy_(good)
+        assert made(x) == (2, 1)                            # k and v; q
+        assert torch.equal(out, want)
