@@ -432,7 +432,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int64_t *slots, in
  *  mask    device uint8 [total_q][max_q], rows mask_stride apart, or NULL.
  *  lse     device FP32 [total_q][q_heads], or NULL.
  *  ws      nvfp4_kv_attention_workspace_bytes(...) bytes, 16-byte aligned, no
- *          initialisation needed; one per stream that runs concurrently.
+ *          initialisation needed; one per stream that runs concurrently. Its
+ *          size depends on the current device's CUs: ask on the device of the
+ *          call.
  * Long sequences are split over the CUs and joined in a fixed order: results
  * are bit-identical from call to call. */
 typedef struct {

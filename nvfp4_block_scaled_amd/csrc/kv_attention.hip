@@ -1341,7 +1341,7 @@ struct Launch {
 // with at most 2 `target` pieces together (each has more steps than a piece, and the steps of all
 // are at most `target` pieces long).
 static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int64_t batch, int64_t max_pages,
-                        int64_t max_q, Launch *L) {
+                        int64_t max_q, int cus, Launch *L) {
   const int64_t G = q_heads / kv.heads, most_rows = max_q * G;
   // One token for each of 64 sequences (10 rows): 22.8 us with 16 rows a workgroup, 34.7 with 32. Three
   // for each of 16 (30 rows): 21.1 with 32, 23.7 in block_kernel. Three to eight for each of 32 (80
@@ -1353,7 +1353,7 @@ static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int6
   // Two workgroups for each CU (64 ragged sequences, 262139 keys: 24.6 and 40 us; one: 26.6 and 47;
   // four: 28 and 46); one where only one is resident (256 queries on 32000 keys of 256 elements: 273 us
   // against 301, 32 drafted trees 49 against 59).
-  const int wgs = L->nt == 8 && kv.D > 128 ? 256 : 512;
+  const int wgs = L->nt == 8 && kv.D > 128 ? cus : 2 * cus;
   L->target = wgs / kv.heads > 0 ? wgs / kv.heads : 1;
   const int64_t steps = ((max_pages << kv.log_p) + kStep - 1) / kStep;
   // Up to 1024 keys are not worth splitting for rows_kernel (731 keys, 4 KV heads: 9.5 us for one
@@ -1433,7 +1433,7 @@ size_t nvfp4_kv_attention_workspace_bytes(const nvfp4_kv_cache *cache, int64_t t
   Launch L;
   if (kv_view(cache, &kv) != NVFP4_OK || check_sizes(kv, total_q, q_heads, batch, max_pages, max_q) != NVFP4_OK) return 0;
   if (max_q > total_q) max_q = total_q > 0 ? total_q : 1;         // as the call does
-  if (!plan_launch(kv, total_q, q_heads, batch, max_pages, max_q, &L)) return 0;
+  if (!plan_launch(kv, total_q, q_heads, batch, max_pages, max_q, device_cus_or_default(), &L)) return 0;
   return workspace_of(kv, L);
 }
 
@@ -1460,7 +1460,7 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache *cache, nvfp4_rows q, int d
     return NVFP4_ERR_ALIGN;
   if (max_q > total_q) max_q = total_q;
   Launch L;
-  if (!plan_launch(A.kv, total_q, q_heads, batch, max_pages, max_q, &L)) return NVFP4_ERR_SHAPE;
+  if (!plan_launch(A.kv, total_q, q_heads, batch, max_pages, max_q, device_cus_or_default(), &L)) return NVFP4_ERR_SHAPE;
   const size_t need = workspace_of(A.kv, L);
   if (need > 0 && (!ws || ws_bytes < need)) return NVFP4_ERR_WORKSPACE;
   if (need > 0 && !aligned(ws, 16)) return NVFP4_ERR_ALIGN;

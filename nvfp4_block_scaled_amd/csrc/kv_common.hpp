@@ -30,6 +30,9 @@ struct KvView {
   __host__ __device__ __forceinline__ uint32_t head_bytes() const { return ((uint32_t)D << log_p) / 8 * 9; }
 };
 
+// CUs of the current device; 256 where there is none (config.hip).
+int device_cus_or_default();
+
 inline bool kv_geometry_ok(int32_t page_size, int32_t kv_heads, int32_t head_dim) {
   return (page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128 || page_size == 256) &&
          kv_heads >= 1 && kv_heads <= 65535 && head_dim >= 16 && head_dim <= 256 && head_dim % 16 == 0;
