@@ -1459,14 +1459,15 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache *cache, nvfp4_rows q, int d
       !aligned(lse, 4))
     return NVFP4_ERR_ALIGN;
   if (max_q > total_q) max_q = total_q;
+  DeviceInfo d;
+  const nvfp4_status on_device = device_info(&d);       // (asked once; arguments are checked without a device too)
   Launch L;
-  if (!plan_launch(A.kv, total_q, q_heads, batch, max_pages, max_q, device_cus_or_default(), &L)) return NVFP4_ERR_SHAPE;
+  if (!plan_launch(A.kv, total_q, q_heads, batch, max_pages, max_q, on_device == NVFP4_OK ? d.num_cus : 256, &L))
+    return NVFP4_ERR_SHAPE;
   const size_t need = workspace_of(A.kv, L);
   if (need > 0 && (!ws || ws_bytes < need)) return NVFP4_ERR_WORKSPACE;
   if (need > 0 && !aligned(ws, 16)) return NVFP4_ERR_ALIGN;
-  DeviceInfo d;
-  st = device_info(&d);
-  if (st != NVFP4_OK) return st;
+  if (on_device != NVFP4_OK) return on_device;
   A.q = (const uint16_t *)q.base, A.q_t = q.token_stride, A.q_h = q.head_stride;
   A.out = (uint16_t *)out.base, A.o_t = out.token_stride, A.o_h = out.head_stride;
   A.lse = lse;
