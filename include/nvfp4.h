@@ -426,7 +426,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int64_t *slots, in
  *  lens    device int32 [batch]: tokens in the cache, the new ones included
  *          (taken as 0 .. max_pages * page_size).
  *  q_start device int32 [batch + 1], ascending, or NULL: one query per sequence
- *          (total_q == batch). Rows that no sequence has are not written.
+ *          (total_q == batch). Rows that no sequence has are not written; where
+ *          q_start does not ascend, what the rows of out and lse get is not
+ *          defined (nothing else is written).
  *  max_q   at least the longest sequence's n; queries of a sequence past it are
  *          not computed. The kernels are chosen by it.
  *  mask    device uint8 [total_q][max_q], rows mask_stride apart, or NULL.

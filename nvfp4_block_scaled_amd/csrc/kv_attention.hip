@@ -102,23 +102,32 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &A, int b) {
 }
 
 // Inclusive prefix sum over a wave: shifts inside rows of 16 lanes, then the rows' last lanes.
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15 into rows 1 and 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31 into rows 2 and 3
+// The sums over sequences are unsigned: those of a q_start that does not ascend may pass 32 bits, and
+// then wrap to numbers that the bounds checks behind them (has_work, join_kernel) turn away.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false);   // row_shr:1
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);   // row_bcast:15 into rows 1 and 3
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);   // row_bcast:31 into rows 2 and 3
   return v;
 }
 
-__device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); }
+__device__ __forceinline__ uint32_t last_lane(uint32_t v) { return lane_of(v, 63); }
 
 // A workgroup's unit: one row tile of one sequence, and one of the `splits` pieces of its keys.
 struct Unit {
-  int b, tile, split, splits, slot;
+  int b, tile, split, splits;
+  uint32_t slot;
   Seq s;
 };
+
+// False only with sequences that overlap in q_start.
+__device__ __forceinline__ bool has_work(const AttnArgs &A, const Unit &u) {
+  return (uint32_t)u.tile < (uint32_t)u.s.row_tiles && (u.splits == 1 || u.slot < (uint32_t)A.slots);
+}
 
 // A lane's sequences from `base` on, PER each: one where a wave's lanes are enough, else four, whose
 // lengths are then on their way together (one token for each of 1024 sequences of 128 keys: 56 us, 80
@@ -140,10 +149,10 @@ __device__ __forceinline__ void shares(const AttnArgs &A, int base, Seq (&s)[PER
 // lose a tenth by it); with more row tiles than workgroups only those several times longer than the
 // average are split. s0: the first 64 PER sequences.
 template <int RT, int PER>
-__device__ __forceinline__ int piece_steps(const AttnArgs &A, Seq (&s0)[PER]) {
+__device__ __forceinline__ uint32_t piece_steps(const AttnArgs &A, Seq (&s0)[PER]) {
   shares<RT, PER>(A, 0, s0);
-  if (A.joins == 0) return 1 << 30;
-  int total = 0, tiles = 0;
+  if (A.joins == 0) return 1u << 30;
+  uint32_t total = 0, tiles = 0;
 #pragma unroll
   for (int i = 0; i < PER; i++) total += s0[i].row_tiles * s0[i].steps, tiles += s0[i].row_tiles;
   for (int base = 64 * PER; base < A.batch; base += 64 * PER) {
@@ -153,52 +162,53 @@ __device__ __forceinline__ int piece_steps(const AttnArgs &A, Seq (&s0)[PER]) {
     for (int i = 0; i < PER; i++) total += s[i].row_tiles * s[i].steps, tiles += s[i].row_tiles;
   }
   total = last_lane(wave_scan(total)), tiles = last_lane(wave_scan(tiles));
-  const int room = RT < kBlockRows ? A.target : max(A.target - tiles / 2, max(1, A.target / 4));
-  return max(1, (total + room - 1) / room);
+  const uint32_t room = RT < kBlockRows ? A.target : max(A.target - (int)(tiles / 2), max(1, A.target / 4));
+  return max(1u, (total + room - 1) / room);
 }
 
-__device__ __forceinline__ int pieces_of(const Seq &s, int chunk) { return max(1, (s.steps + chunk - 1) / chunk); }
+__device__ __forceinline__ uint32_t pieces_of(const Seq &s, uint32_t chunk) { return max(1u, (s.steps + chunk - 1) / chunk); }
 
-// Finds unit `u`; false past the last. Every wave does it for itself with no exchange through memory:
-// a prefix sum over the sequences' pieces says whose piece `u` is. REVERSE: of a sequence under the
+// Finds unit `unit`; false past the last. Every wave does it for itself with no exchange through memory:
+// a prefix sum over the sequences' pieces says whose piece it is. REVERSE: of a sequence under the
 // causal mask, the last row tile comes first: it sees the most keys.
 template <int RT, bool REVERSE, int PER>
-__device__ __forceinline__ bool find_unit_per(const AttnArgs &A, int u, Unit *out) {
+__device__ __forceinline__ bool find_unit_per(const AttnArgs &A, int unit, Unit *out) {
   Seq s[PER];
-  const int chunk = piece_steps<RT, PER>(A, s);
-  int units = 0, slots = 0;
+  const uint32_t chunk = piece_steps<RT, PER>(A, s), u = unit;
+  uint32_t units = 0, slots = 0;
   for (int base = 0; base < A.batch; base += 64 * PER) {
     if (base > 0) shares<RT, PER>(A, base, s);
-    int n[PER], mine = 0, part = 0;
+    uint32_t n[PER], mine = 0, part = 0;
 #pragma unroll
     for (int i = 0; i < PER; i++) {
       n[i] = pieces_of(s[i], chunk);
       mine += s[i].row_tiles * n[i];
       part += n[i] > 1 ? s[i].row_tiles * n[i] : 0;
     }
-    const int to = units + wave_scan(mine), slot_to = slots + wave_scan(part);
+    const uint32_t to = units + wave_scan(mine), slot_to = slots + wave_scan(part);
     const uint64_t hit = __ballot(u < to);
     if (hit) {
       const int at = __builtin_ctzll(hit);
-      int first = __builtin_amdgcn_readlane(to - mine, at), slot = __builtin_amdgcn_readlane(slot_to - part, at);
+      uint32_t first = lane_of(to - mine, at), slot = lane_of(slot_to - part, at);
       bool found = false;
 #pragma unroll
       for (int i = 0; i < PER; i++) {
-        const int tiles = __builtin_amdgcn_readlane(s[i].row_tiles, at), splits = __builtin_amdgcn_readlane(n[i], at);
-        const int count = tiles * splits;
+        const uint32_t tiles = lane_of(s[i].row_tiles, at), splits = lane_of(n[i], at);
+        const uint32_t count = tiles * splits;
         if (!found && (i == PER - 1 || u < first + count)) {
           found = true;
+          const uint32_t tile = (u - first) / splits;
           out->b = base + at * PER + i;
           out->splits = splits;
-          out->tile = (u - first) / splits;
-          out->split = (u - first) - out->tile * splits;
+          out->tile = tile;
+          out->split = (u - first) - tile * splits;
           out->slot = slot + u - first;
-          out->s.len = __builtin_amdgcn_readlane(s[i].len, at);
-          out->s.queries = __builtin_amdgcn_readlane(s[i].queries, at);
-          out->s.first = __builtin_amdgcn_readlane(s[i].first, at);
+          out->s.len = lane_of(s[i].len, at);
+          out->s.queries = lane_of(s[i].queries, at);
+          out->s.first = lane_of(s[i].first, at);
           out->s.row_tiles = tiles;
-          out->s.steps = __builtin_amdgcn_readlane(s[i].steps, at);
-          if (REVERSE && A.causal) out->tile = tiles - 1 - out->tile;
+          out->s.steps = lane_of(s[i].steps, at);
+          if (REVERSE && A.causal) out->tile = tiles - 1 - tile;
         }
         first += count;
         if (splits > 1) slot += count;
@@ -241,18 +251,19 @@ __device__ __forceinline__ void list_joins(const AttnArgs &A) {
   if (threadIdx.x >= 64) return;
   const int lane = threadIdx.x;
   Seq one[1];
-  const int chunk = piece_steps<RT, 1>(A, one);
-  int slots = 0, joins = 0;
+  const uint32_t chunk = piece_steps<RT, 1>(A, one);
+  uint32_t slots = 0, joins = 0;
   for (int base = 0; base < A.batch; base += 64) {
     if (base > 0) shares<RT, 1>(A, base, one);
     const Seq &s = one[0];
-    const int n = pieces_of(s, chunk);
+    const uint32_t n = pieces_of(s, chunk);
     const int tiles = n > 1 ? s.row_tiles : 0;
-    const int slot_to = slots + wave_scan(tiles * n), join_to = joins + wave_scan(tiles);
+    const uint32_t slot_to = slots + wave_scan(tiles * n), join_to = joins + wave_scan(tiles);
     const int rows = min(s.queries, A.max_q) * A.group;
     for (int i = 0; i < tiles; i++) {
-      const int j = join_to - tiles + i, tile = REVERSE && A.causal ? tiles - 1 - i : i;
-      if (j >= A.joins) break;
+      const uint32_t j = join_to - tiles + i;
+      const int tile = REVERSE && A.causal ? tiles - 1 - i : i;
+      if (j >= (uint32_t)A.joins) break;
       A.joins_at[4 * j] = s.first * A.group + tile * RT;          // (query, head of the group) row
       A.joins_at[4 * j + 1] = min(rows - tile * RT, RT);
       A.joins_at[4 * j + 2] = slot_to - tiles * n + i * n;
@@ -260,7 +271,7 @@ __device__ __forceinline__ void list_joins(const AttnArgs &A) {
     }
     slots = last_lane(slot_to), joins = last_lane(join_to);
   }
-  if (lane == 0) *A.join_count = min(joins, A.joins);
+  if (lane == 0) *A.join_count = min(joins, (uint32_t)A.joins);
 }
 
 // The keys that query i of a sequence sees: [lo, hi) (under a tree mask, those before the new ones).
@@ -485,8 +496,7 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
   Unit unit;
   if (!find_unit<RT, false>(A, u, &unit)) return;
   const Seq &s = unit.s;
-  // (only with sequences that overlap in q_start)
-  if (unit.tile < 0 || unit.tile >= s.row_tiles || (unit.splits > 1 && unit.slot >= A.slots)) return;
+  if (!has_work(A, unit)) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int D = kv.D, G = A.group;
@@ -852,7 +862,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void block_kernel(const Att
   Unit unit;
   if (!find_unit<RT, true>(A, u, &unit)) return;
   const Seq &s = unit.s;
-  if (unit.tile < 0 || unit.tile >= s.row_tiles || (unit.splits > 1 && unit.slot >= A.slots)) return;
+  if (!has_work(A, unit)) return;
   const int lane = threadIdx.x & 63, m = lane & 31, hi = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int D = kv.D, G = A.group;
@@ -1261,7 +1271,8 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs A, int groups)
   const int count = *A.join_count;
   const int row0 = A.joins_at[4 * j], rows = A.joins_at[4 * j + 1], slot = A.joins_at[4 * j + 2], splits = A.joins_at[4 * j + 3];
   if (j >= count) return;
-  if (group * ROWS >= rows || slot + splits > A.slots) return;
+  // (the second only with sequences that overlap in q_start)
+  if (group * ROWS >= rows || (uint32_t)slot >= (uint32_t)A.slots || splits > A.slots - slot) return;
   const int D = kv.D, G = A.group;
   const int sl = threadIdx.x / TH, d = (threadIdx.x % TH) * 4;
   const int n = group * ROWS + sl / SL, part = sl % SL;

@@ -204,3 +204,32 @@ def test_inputs_the_kernels_cannot_read_are_copied_once():
         x.copy_(good)
         assert made(x) == (2, 1)                            # k and v; q
         assert torch.equal(out, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,T,n", [(6, 40, 600), (1030, 8192, 1 << 20), (1100, 700, 1 << 20)])
+@pytest.mark.parametrize("heads", [2, 16])
+def test_sequences_that_overlap_in_q_start_stay_in_bounds(batch, T, n, heads):
+    """q_start has to ascend. Where it does not, sums over sequences pass 32 bits in the second size; what is written
+    is not defined then, but nothing outside the outputs and the workspace is, and the next call is right."""
+    P, D = 256, 16
+    pages = torch.zeros((2, nv.nvfp4_kv_page_bytes(P, 1, D)), dtype=torch.uint8, device="cuda")
+    cache = nv.KVCache(pages, P, 1, D)
+    table = torch.ones((batch, -(-n // P)), dtype=torch.int32, device="cuda")
+    lens = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    start = torch.zeros(batch + 1, dtype=torch.int32, device="cuda")
+    start[1::2] = T
+    q = torch.ones((T, heads, D), dtype=torch.bfloat16, device="cuda")
+    room = 1 << 16
+    out, lse = torch.full((T * heads * D + 2 * room,), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((T * heads + 2 * room,), 7.0, device="cuda")
+    size = nv.nvfp4_kv_attention_workspace(T, heads, cache, batch, table.shape[1], T).numel()
+    ws = torch.full((size + 2 * room,), 7, dtype=torch.uint8, device="cuda")
+    args = dict(out=out[room:-room].view(T, heads, D), lse=lse[room:-room].view(T, heads), ws=ws[room:-room])
+    nv.nvfp4_kv_attention(q, cache, table, lens, start, T, **args)
+    torch.cuda.synchronize()
+    for t in (out, lse, ws):
+        assert bool((t[:room] == 7).all()) and bool((t[-room:] == 7).all())
+    start = torch.full((batch + 1,), T, dtype=torch.int32, device="cuda")
+    start[0] = 0
+    nv.nvfp4_kv_attention(q, cache, table, lens, start, T, causal=False, **args)
+    assert not args["out"].any() and bool(((args["lse"] - math.log(n)).abs() < 1e-5).all())
