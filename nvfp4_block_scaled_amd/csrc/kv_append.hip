@@ -79,12 +79,11 @@ __device__ __forceinline__ bool find_slot(const KvView &kv, int64_t slot, uint8_
 // The elements that a thread turns or passes on: a[j], b[j] of pair 8 c + j, or (c past the turned
 // ones) sixteen consecutive elements. As loaded, 16 bytes wide (VEC: rot is a multiple of 16), or
 // one by one.
-template <bool VEC>
 struct Part {
   u32x4_t lo, hi;
 };
 
-template <bool VEC, bool INTER>
+template <bool INTER>
 __device__ __forceinline__ void part_at(int c, int D, int rot, int turn_chunks, int j, int *ea, int *eb, bool *fa, bool *fb) {
   const int half = rot / 2, p = 8 * c + j, e = rot + 16 * (c - turn_chunks) + j;
   const bool turn = c < turn_chunks;
@@ -94,19 +93,19 @@ __device__ __forceinline__ void part_at(int c, int D, int rot, int turn_chunks, 
   *fb = turn ? p < half : e + 8 < D;
 }
 
-template <bool VEC, bool INTER>
+template <bool INTER>
 __device__ __forceinline__ void first_of(int c, int rot, int turn_chunks, int *ea, int *eb) {
   const bool turn = c < turn_chunks;
   *ea = !turn ? rot + 16 * (c - turn_chunks) : INTER ? 16 * c : 8 * c;
   *eb = (turn && !INTER) ? rot / 2 + 8 * c : *ea + 8;
 }
 
-template <bool F16, bool VEC, bool INTER>
-__device__ __forceinline__ Part<VEC> load_part(const uint16_t *x, int c, int D, int rot, int turn_chunks) {
-  Part<VEC> r;
+template <bool VEC, bool INTER>
+__device__ __forceinline__ Part load_part(const uint16_t *x, int c, int D, int rot, int turn_chunks) {
+  Part r;
   if (VEC) {
     int ea, eb;
-    first_of<VEC, INTER>(c, rot, turn_chunks, &ea, &eb);
+    first_of<INTER>(c, rot, turn_chunks, &ea, &eb);
     r.lo = *reinterpret_cast<const u32x4_t *>(x + ea);
     r.hi = *reinterpret_cast<const u32x4_t *>(x + eb);
   } else {
@@ -115,7 +114,7 @@ __device__ __forceinline__ Part<VEC> load_part(const uint16_t *x, int c, int D, 
     for (int j = 0; j < 8; j++) {
       int ea, eb;
       bool fa, fb;
-      part_at<VEC, INTER>(c, D, rot, turn_chunks, j, &ea, &eb, &fa, &fb);
+      part_at<INTER>(c, D, rot, turn_chunks, j, &ea, &eb, &fa, &fb);
       a[j] = fa ? x[ea] : 0;
       b[j] = fb ? x[eb] : 0;
     }
@@ -131,7 +130,7 @@ __device__ __forceinline__ Part<VEC> load_part(const uint16_t *x, int c, int D, 
 // Turns a part: x[0..7] and y[0..7] in the order in which they are stored (VEC: at first_of's two
 // places; else a and b of part_at).
 template <bool F16, bool VEC, bool INTER>
-__device__ __forceinline__ void turn_part(const Part<VEC> &r, bool turn, const float (&cs)[8], const float (&sn)[8],
+__device__ __forceinline__ void turn_part(const Part &r, bool turn, const float (&cs)[8], const float (&sn)[8],
                                           float (&x)[8], float (&y)[8]) {
   unpack8<F16>(r.lo, x);
   unpack8<F16>(r.hi, y);
@@ -258,10 +257,10 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(const AppendArgs
     uint16_t *dst = A.q_out + t * A.o_t;
     const int h0 = group * A.per_group, h1 = min(A.q_heads, h0 + A.per_group);
     for (int hb = h0; hb < h1; hb += BATCH) {
-      Part<VEC> r[BATCH];
+      Part r[BATCH];
 #pragma unroll
       for (int i = 0; i < BATCH; i++)
-        r[i] = load_part<F16, VEC, INTER>(src + min(hb + i, h1 - 1) * A.q_h, c, D, A.rot, A.turn_chunks);
+        r[i] = load_part<VEC, INTER>(src + min(hb + i, h1 - 1) * A.q_h, c, D, A.rot, A.turn_chunks);
 #pragma unroll
       for (int i = 0; i < BATCH; i++) {
         if (hb + i >= h1) break;
@@ -270,7 +269,7 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(const AppendArgs
         uint16_t *o = dst + (hb + i) * A.o_h;
         if (VEC) {
           int ea, eb;
-          first_of<VEC, INTER>(c, A.rot, A.turn_chunks, &ea, &eb);
+          first_of<INTER>(c, A.rot, A.turn_chunks, &ea, &eb);
           *reinterpret_cast<u32x4_t *>(o + ea) = pack8<F16>(x);
           *reinterpret_cast<u32x4_t *>(o + eb) = pack8<F16>(y);
         } else {
@@ -278,7 +277,7 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(const AppendArgs
           for (int j = 0; j < 8; j++) {
             int ea, eb;
             bool fa, fb;
-            part_at<VEC, INTER>(c, D, A.rot, A.turn_chunks, j, &ea, &eb, &fa, &fb);
+            part_at<INTER>(c, D, A.rot, A.turn_chunks, j, &ea, &eb, &fa, &fb);
             if (fa) o[ea] = pack1<F16>(x[j]);
             if (fb) o[eb] = pack1<F16>(y[j]);
           }
@@ -298,12 +297,12 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(const AppendArgs
   for (int h = group * A.per_group; h < h1; h++) {
     if (active) {
       float x[8], y[8];
-      turn_part<F16, VEC, INTER>(load_part<F16, VEC, INTER>(A.k + t * A.k_t + h * A.k_h, c, D, A.rot, A.turn_chunks), turn,
+      turn_part<F16, VEC, INTER>(load_part<VEC, INTER>(A.k + t * A.k_t + h * A.k_h, c, D, A.rot, A.turn_chunks), turn,
                                  cs, sn, x, y);
       float *row = turned + tl * D;
       if (VEC) {
         int ea, eb;
-        first_of<VEC, INTER>(c, A.rot, A.turn_chunks, &ea, &eb);
+        first_of<INTER>(c, A.rot, A.turn_chunks, &ea, &eb);
         *reinterpret_cast<f32x4_t *>(row + ea) = f32x4_t{x[0], x[1], x[2], x[3]};
         *reinterpret_cast<f32x4_t *>(row + ea + 4) = f32x4_t{x[4], x[5], x[6], x[7]};
         *reinterpret_cast<f32x4_t *>(row + eb) = f32x4_t{y[0], y[1], y[2], y[3]};
@@ -313,7 +312,7 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(const AppendArgs
         for (int j = 0; j < 8; j++) {
           int ea, eb;
           bool fa, fb;
-          part_at<VEC, INTER>(c, D, A.rot, A.turn_chunks, j, &ea, &eb, &fa, &fb);
+          part_at<INTER>(c, D, A.rot, A.turn_chunks, j, &ea, &eb, &fa, &fb);
           if (fa) row[ea] = x[j];
           if (fb) row[eb] = y[j];
         }

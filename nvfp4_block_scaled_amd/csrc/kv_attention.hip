@@ -341,10 +341,9 @@ __device__ __forceinline__ Buffer head_buffer(const KvView &kv, int page, int64_
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, kv.head_bytes(), 0x00027000);
 }
 
-template <int N>
-__device__ __forceinline__ uint32_t load_bytes(const uint8_t *p) {
+// A pair of scales, at any byte.
+__device__ __forceinline__ uint32_t load_pair(const uint8_t *p) {
   uint16_t h;
-  static_assert(N == 2, "a pair of scales");
   __builtin_memcpy(&h, p, 2);
   return h;
 }
@@ -955,7 +954,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void block_kernel(const Att
       const uint8_t *p = m < 16 ? p0 : p1;
       const uint32_t at = (uint32_t)key & (kv.P() - 1u);
       t.kw = *reinterpret_cast<const u32x4_a4 *>(p + at * (uint32_t)(D / 2) + k_off);
-      t.ks = load_bytes<2>(p + at * blocks + ks_off);
+      t.ks = load_pair(p + at * blocks + ks_off);
     }
     if (v_task) {
       const int token = base + 4 * tg;

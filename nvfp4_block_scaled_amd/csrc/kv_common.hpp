@@ -99,16 +99,6 @@ __device__ __forceinline__ uint16_t pack1(float x) {
 }
 
 template <bool F16>
-__device__ __forceinline__ float unpack1(uint16_t u) {
-  if (F16) {
-    _Float16 h;
-    __builtin_memcpy(&h, &u, 2);
-    return (float)h;
-  }
-  return __uint_as_float((uint32_t)u << 16);
-}
-
-template <bool F16>
 __device__ __forceinline__ u32x4_t pack8(const float (&x)[8]) {
   u32x4_t w;
 #pragma unroll
