@@ -438,7 +438,14 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int64_t *slots, in
  *          size depends on the current device's CUs: ask on the device of the
  *          call.
  * Long sequences are split over the CUs and joined in a fixed order: results
- * are bit-identical from call to call. */
+ * are bit-identical from call to call. How far they are split, the workspace
+ * and the second launch follow max_pages, not the lengths, which the host does
+ * not know: a table wider than its sequences costs a launch that finds less to
+ * do.
+ * Scores, maxima and sums are FP32. The weights e^(t_j - m) are rounded to FP16
+ * (2^-11 of each, independently) before they meet the values: with out in BF16
+ * that does not show beside its own rounding, in F16 it adds about a quarter to
+ * the error. */
 typedef struct {
   float scale;              /* finite, > 0 */
   int32_t causal;           /* 0 or 1 */

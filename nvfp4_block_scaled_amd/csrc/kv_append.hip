@@ -8,8 +8,10 @@
 //
 // Bound by memory: q, k and v come in once and q goes out once (the cache's 9/16
 // of a byte per element is small beside them): 8192 tokens of 40 + 2 x 4 heads of
-// 128 (195 MB) take 41.7 us, 4.7 TB/s, the rate of a large copy; 64 tokens (1.5 MB)
-// 4.8 us and a read-back of them 4.5, a launch each. A thread owns eight pairs of one
+// 128 (195 MB) take 41.5 us, 4.7 TB/s, the rate of a large copy; 64 tokens (1.5 MB)
+// 4.7 us and a read-back of them 4.6, a launch each. Where rot is no multiple of 16, elements
+// move two bytes at a time: 8192 tokens of 48 heads of 80, 40 of them turned (119 MB), take 117 us,
+// 1.0 TB/s. A thread owns eight pairs of one
 // token: their cosines and sines stay in registers over the heads of its group,
 // so the table is read once per group and not once per head. A turned key head
 // goes through LDS, because the pairs (j, j + rot/2) of one thread lie in two
@@ -471,9 +473,9 @@ nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache *cache, nvfp4_rows k, nvfp4_ro
   const int per_wg = kAppendThreads / A.chunks;
   const int64_t wgs = (tokens + per_wg - 1) / per_wg;
   if (wgs > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
-  // Sixteen heads to a group share one read of the table (8192 tokens of 48 heads: 54.2 us with the
-  // read-back, 55.9 with eight); with few tokens, fewer heads to a group fill the CUs instead (64
-  // tokens: 14 workgroups of eight heads each took 13.7 us, 96 of one take 3.4).
+  // Sixteen heads to a group share one read of the table (8192 tokens of 48 heads, replayed in a graph:
+  // 33.3 us, 35.3 with eight); with few tokens, fewer heads to a group fill the CUs instead (64 tokens:
+  // 4.3 us with one, 5.8 with two, 8.8 with four to sixteen).
   int groups;
   for (A.per_group = 16;; A.per_group /= 2) {
     A.q_groups = (A.q_heads + A.per_group - 1) / A.per_group;

@@ -61,7 +61,8 @@ struct AttnArgs {
 };
 
 // Asks for the arguments' cache lines before the first is needed: left alone, each line is a wait of
-// its own, some of them at the kernel's end (32 sequences of 3 to 8 queries: 34.9 -> 34.5 us).
+// its own, some of them at the kernel's end (256 queries on 32000 keys: 220.3 -> 218.6 us, 64 for each of 16
+// sequences of 8000: 279.9 -> 276.5; drafted trees and single tokens: no difference).
 template <typename T>
 __device__ __forceinline__ void touch(T v) {
   asm volatile("" ::"s"(v));
@@ -130,8 +131,8 @@ __device__ __forceinline__ bool has_work(const AttnArgs &A, const Unit &u) {
 }
 
 // A lane's sequences from `base` on, PER each: one where a wave's lanes are enough, else four, whose
-// lengths are then on their way together (one token for each of 1024 sequences of 128 keys: 56 us, 80
-// with one to a lane, 63 with eight; 128 sequences: 22.6, 22.4, 23.6).
+// lengths are then on their way together (one token for each of 1024 sequences of 128 keys: 51.8 us, 54.5
+// with one to a lane, 58.0 with eight; 128 sequences of up to 4096: 24.6, 24.1, 26.3).
 template <int RT, int PER>
 __device__ __forceinline__ void shares(const AttnArgs &A, int base, Seq (&s)[PER]) {
 #pragma unroll
@@ -144,10 +145,11 @@ __device__ __forceinline__ void shares(const AttnArgs &A, int base, Seq (&s)[PER
 
 // How many steps a piece has: the call's steps over the workgroups to fill. For block_kernel, whose
 // workgroups are long, half a workgroup for each row tile is set aside, so that all pieces run in one
-// round, short last ones included (256 queries on 32000 keys: 308 us without, 228 with; 64 on each of
-// 16 sequences: 115 without, 111 with half, 154 with a whole one; rows_kernel's are short and many, and
-// lose a tenth by it); with more row tiles than workgroups only those several times longer than the
-// average are split. s0: the first 64 PER sequences.
+// round, short last ones included (256 queries on 32000 keys: 299 us without, 219 with half, 223 with a
+// whole one; 32 drafted trees with heads of 256: 85, 69, 94; 64 queries on each of 16 sequences of 8000
+// keys: 277, 277, 309). rows_kernel's are short and many (64 ragged sequences: 22.2 us without, 23.6 with;
+// three queries for each of 16: 23.5, 24.8; 128 ragged sequences: 24.6, 22.8). With more row tiles than
+// workgroups only those several times longer than the average are split. s0: the first 64 PER sequences.
 template <int RT, int PER>
 __device__ __forceinline__ uint32_t piece_steps(const AttnArgs &A, Seq (&s0)[PER]) {
   shares<RT, PER>(A, 0, s0);
@@ -472,9 +474,9 @@ __device__ __forceinline__ float query_scale(float top, float *up) {
 // present one is computed.
 //
 // Bound by the cache's bytes where there are many: one token on 262139 keys (151 MB, 4 heads of 128):
-// 32.8 us here and 6.3 in join_kernel, 4.6 TB/s of the 6.0 that a plain read reaches; one token for each
-// of 64 ragged sequences (54 MB): 19 + 4.9 us, of which about ten pass before the first tile is there and
-// after the last one. A single sequence of 731 keys (0.4 MB): 9.5 us, all latency; a launch that does
+// 32.5 us here and 6.0 in join_kernel, 4.6 TB/s of the 6.0 that a plain read reaches; one token for each
+// of 64 ragged sequences (54 MB): 18.8 + 4.8 us, of which about ten pass before the first tile is there and
+// after the last one. A single sequence of 731 keys (0.4 MB): 9.6 us, all latency; a launch that does
 // nothing but find no unit takes 5.6. 8 or 16 waves a workgroup, non-temporal loads and contiguous
 // shares of the waves measured slower or the same.
 template <int DP, int NT, bool F16, bool ODD>
@@ -796,16 +798,16 @@ __global__ __launch_bounds__(256, NT == 1 && DP <= 128 ? 3 : 2) void rows_kernel
 // way into registers, and they are dequantized into the other buffer before the one barrier of a
 // tile.
 //
-// Chunks of up to 2048 queries of 40 heads on 4 sequences of up to 8192 keys (508 GFLOP): 600 to 640 us,
-// 0.79 to 0.85 PFLOP/s (a plain 8192^3 product: 1.27). No unit is full: the matrix cores are busy a
-// third of the cycles, the vector units 55 % (350 instructions a wave and tile, of which a third is
-// the softmax and a quarter dequantizing), LDS 30 %; the two waves of a SIMD wait for data, barriers
+// Chunks of up to 2048 queries of 40 heads on 4 sequences of up to 8192 keys (508 GFLOP): 591 to 606 us,
+// 0.84 to 0.86 PFLOP/s (a plain 8192^3 product: 1.27). No unit is full: the matrix cores are busy a
+// third of the cycles, the vector units 56 % (350 instructions a wave and tile, of which a third is
+// the softmax and a quarter dequantizing), LDS 31 %; the two waves of a SIMD wait for data, barriers
 // and each other for the rest. Measured and not better: the next tile's dequantizing among the first
 // product's steps (620 against 605), fragments read ahead in the second product too (640 against 636),
 // codes two tiles ahead (600 against 606, for twice the code), tiles of 32 keys with three waves a SIMD
-// (834 against 600). At D > 128 a lane's sums and queries take 192 registers, and two waves a SIMD
-// would spill: one workgroup a CU then (chunks of 2048 queries on 8192 keys of 256 elements, 307 GFLOP:
-// 667 us, 888 with two that spill).
+// (834 against 600). At D > 128 a lane's sums and queries take 192 registers; two waves a SIMD spill 51
+// of 256, and win nothing by it (2048 queries of 8 heads of 256 on 4 x 8192 keys, 481 GFLOP: 921 us with one
+// workgroup a CU, 912 with two; 256 on 32000 keys 146 and 144; 32 drafted trees 68.4 and 68.8): one is kept.
 template <int DP>
 struct Block {
   static constexpr int KT = DP == 256 ? 32 : 64;       // keys of a tile (LDS: 64 KiB at D >= 128)
@@ -1353,21 +1355,22 @@ struct Launch {
 static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int64_t batch, int64_t max_pages,
                         int64_t max_q, int cus, Launch *L) {
   const int64_t G = q_heads / kv.heads, most_rows = max_q * G;
-  // One token for each of 64 sequences (10 rows): 22.8 us with 16 rows a workgroup, 34.7 with 32. Three
-  // for each of 16 (30 rows): 21.1 with 32, 23.7 in block_kernel. Three to eight for each of 32 (80
-  // rows): 34 in block_kernel, 38 with 96 rows in rows_kernel.
+  // One token for each of 64 sequences (10 rows): 22.2 us with 16 rows a workgroup, 33.1 with 32. Three
+  // for each of 16 sequences of 4000 keys (30 rows): 23.5 with 32, 32.6 in block_kernel. Three to eight for
+  // each of 32 (80 rows): 32.6 in block_kernel, 209 with 96 rows in rows_kernel, which spills.
   L->nt = most_rows <= 16 ? 1 : most_rows <= 32 && kv.D <= 128 ? 2 : 8;
   const int64_t RT = 16 * L->nt;
   const int64_t by_seq = batch * ((most_rows + RT - 1) / RT), by_rows = total_q * G / RT + batch;
   const int64_t tiles = by_seq < by_rows ? by_seq : by_rows;
-  // Two workgroups for each CU (64 ragged sequences, 262139 keys: 24.6 and 40 us; one: 26.6 and 47;
-  // four: 28 and 46); one where only one is resident (256 queries on 32000 keys of 256 elements: 273 us
-  // against 301, 32 drafted trees 49 against 59).
+  // Two workgroups for each CU (64 ragged sequences, 262139 keys: 22.2 and 33.3 us; one: 24.7 and 37.2;
+  // three: 24.7 and 35.8; four: 24.3 and 38.4); one where only one is resident (256 queries of 8 heads of 256
+  // on 32000 keys: 146 us against 155, 32 drafted trees 69 against 74).
   const int wgs = L->nt == 8 && kv.D > 128 ? cus : 2 * cus;
   L->target = wgs / kv.heads > 0 ? wgs / kv.heads : 1;
   const int64_t steps = ((max_pages << kv.log_p) + kStep - 1) / kStep;
-  // Up to 1024 keys are not worth splitting for rows_kernel (731 keys, 4 KV heads: 9.5 us for one
-  // workgroup a head, 9.9 with pieces joined in a second launch, which costs the host 3 us more).
+  // Up to 1024 keys are not worth splitting for rows_kernel, whose second launch costs the host 2 us (a
+  // token on 731 keys: 10.5 us a call in one workgroup a head, 12.7 in pieces; one for each of 1024
+  // sequences of 128 keys: 51.8, 71.7). The table's width stands for the keys: the lengths are on the device.
   if (steps > (L->nt < 8 ? 8 : 1)) {
     L->joins = tiles < L->target ? tiles : L->target;
     const int64_t most = tiles * steps, slots = 2 * (int64_t)L->target;
@@ -1379,7 +1382,7 @@ static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int6
   }
   // A workgroup of join_kernel takes eight rows (at D = 128) where there are many row tiles of few
   // pieces, two with four times as many pieces in flight where there are few of many (one sequence of
-  // 8000 keys and 8 queries, 63 pieces: 20.8 us against 28; 32 drafted trees: 38.6 against 35).
+  // 8000 keys and 8 queries, 63 pieces: 21.2 us against 28.2; 32 drafted trees: 36.0 against 32.6).
   const int DP = kv.D <= 64 ? 64 : kv.D <= 128 ? 128 : 256;
   L->few = L->joins * kv.heads <= 32;
   const int in_join = L->nt < 8 ? 1 : (L->few ? 256 : 1024) / DP;

@@ -7,9 +7,9 @@
 //
 // Copying is bound by memory: every page byte is read once and written once, 16
 // bytes a lane, four loads in flight per lane: a fork that copies 302 MB takes
-// 50.9 us (5.9 TB/s: shared sources come from the caches), a compaction that moves
-// 283 MB 58.2 us (4.9 TB/s; a large copy: 4.7). The bookkeeping is bound by the
-// latency of a few dependent passes over the counts: 5 to 6 us before a copy, 11.3
+// 51.2 us (5.9 TB/s: shared sources come from the caches), a compaction that moves
+// 283 MB 57.5 us (4.9 TB/s; a large copy: 4.7). The bookkeeping is bound by the
+// latency of a few dependent passes over the counts: 5 to 7 us before a copy, 11.3
 // for a resize of 256 sequences in a pool of 65536 pages (three launches).
 #include "kv_common.hpp"
 

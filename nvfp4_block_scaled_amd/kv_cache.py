@@ -258,7 +258,8 @@ def nvfp4_kv_attention(q, cache, table, lens, q_start=None, max_q=None, scale=No
     longest sequence's queries (None: total_q). scale: 1 / sqrt(head_dim) by default. window > 0:
     each query sees the last `window` keys up to its own. mask: bool or uint8 [total_q][>= max_q], which
     of the sequence's new tokens a query sees (drafted trees; replaces causal). Returns out, or (out,
-    lse) with lse float32 [total_q][q_heads]. A query that sees no key gets zeros and -inf."""
+    lse) with lse float32 [total_q][q_heads]. A query that sees no key gets zeros and -inf; a row past the
+    last sequence's is left as it was. How far sequences are split follows the table's width, not lens."""
     dev = _device()
     c = _cache(cache, dev)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
