@@ -45,7 +45,8 @@ def reference(q, k, v, scale, see, lost=()):
 def worst(got, want, bound, dtype):
     """The largest error over its bound, the output's rounding included."""
     u, least = (2.0 ** -8, 0.0) if dtype == "bf16" else (2.0 ** -11, 2.0 ** -25)
-    return float((np.abs(got - want) / (bound * (1 + u) + u * np.abs(want) + least)).max())
+    err, tol = np.abs(got - want), bound * (1 + u) + u * np.abs(want) + least
+    return float(np.divide(err, tol, out=np.zeros_like(err), where=err != 0).max())     # (no error where none may be: 0)
 
 
 def case(seed, lens, counts, hq, hkv, D, P, dtype):
@@ -92,6 +93,25 @@ def test_split_sequences_within_the_bound(D, P, n, name, counts, hq, hkv, dtype)
     for rows, heads, q, k, v, see in parts:
         want, w_lse, bound, l_bound = reference(q, k, v, 1 / math.sqrt(D), see)
         assert worst(out[rows, heads].reshape(want.shape), want, bound, dtype) <= 1.0
+        assert (np.abs(lse[rows, heads].reshape(-1) - w_lse) <= l_bound).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("extra", [0, 1, 40, 2000])
+@pytest.mark.parametrize("counts", [[1, 1, 1], [9, 1, 30]])
+def test_tables_wider_than_their_sequences(extra, counts):
+    """A captured step's table has room for the longest context it may meet; the unused columns hold any id."""
+    D, P, lens = 128, 16, [300, 1, 77]
+    pages, table, k_g, v_g, qt, parts = case(5, lens, counts, 8, 2, D, P, "bf16")
+    table = np.concatenate([table, synth.rng(extra).integers(-5, 99, (3, extra)).astype(np.int32)], 1)
+    cache = nv.KVCache(dev(pages), P, 2, D, dev(k_g), dev(v_g))
+    start = dev(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)) if max(counts) > 1 else None
+    out, lse = nv.nvfp4_kv_attention(qt.cuda(), cache, dev(table), dev(np.array(lens, np.int32)), start, max(counts),
+                                     return_lse=True)
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for rows, heads, q, k, v, see in parts:
+        want, w_lse, bound, l_bound = reference(q, k, v, 1 / math.sqrt(D), see)
+        assert worst(out[rows, heads].reshape(want.shape), want, bound, "bf16") <= 1.0
         assert (np.abs(lse[rows, heads].reshape(-1) - w_lse) <= l_bound).all()
 
 
