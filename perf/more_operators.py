@@ -275,7 +275,7 @@ def _own(op, s):
     if op == "dispatch":
         offsets, tokens, places = nv.nvfp4_moe_sort(s["ids"], c["experts"])
         out = {"offsets": offsets, "tokens": tokens, "places": places,
-               "rows": nv.nvfp4_moe_gather(s["x"], tokens, out=s["rows"])}
+               "rows": nv.nvfp4_moe_gather(s["x"], places, out=s["rows"])}
         if c["back"]:
             out["grad_x"] = nv.nvfp4_moe_gather_backward(s["grad"], places)
         return out
