@@ -9,7 +9,9 @@
  *   W4A16: y[m][n] = alpha * sum_k  x[m][k] * (W[n][k] * SFW[n][k/16])
  *
  * and, for the attention between two such layers, a key/value cache in the same
- * format (nvfp4_kv_*: append with rotary positions, read, attention, pages).
+ * format (nvfp4_kv_*: append with rotary positions, read, attention, pages), and,
+ * for layers held in FP8 and for experts, FP8 products with block scales
+ * (nvfp4_fp8_*) and the way of tokens to experts and back (nvfp4_moe_*).
  *
  * A, B, W hold 4-bit E2M1 codes packed two per byte along K (element 2j in the
  * low nibble of byte j); SFA, SFB, SFW hold one E4M3 (or UE4M3) scale byte per
@@ -512,6 +514,99 @@ nvfp4_status nvfp4_kv_resize(int64_t num_pages, int32_t page_size, const int32_t
 nvfp4_status nvfp4_kv_compact(const nvfp4_kv_pool *pool, const int32_t *table, int64_t table_stride, int64_t width,
                               int64_t batch, const int32_t *refs, int32_t *table_out, int64_t table_out_stride,
                               int32_t *refs_out, int32_t *live_dev, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * FP8 matrices in blocks, and the experts' operators.
+ *
+ * A matrix in FP8 holds E4M3 codes with one FP32 scale per block: a value
+ * stands for code * scale. An activation [M][K] has a scale for each 128
+ * consecutive values of a row, [M][ceil(K/128)]; a weight [N][K] one for each
+ * 128 x 128 block, [ceil(N/128)][ceil(K/128)]. Codes are row-major bytes, rows
+ * K bytes apart, 16-byte aligned; K % 16 == 0. Nothing is prepared or laid out
+ * anew: the products read the codes as they are. */
+
+/* BF16, FP16 or FP32 rows -> FP8 rows.
+ *  x      [rows][K] of dtype (nvfp4_dtype), rows ldx elements apart; with gated,
+ *         [rows][2K]: columns 0 .. K-1 are a gate g, K .. 2K-1 a factor u, and
+ *         silu(g) u = g / (1 + e^-g) u, in FP32, is quantized.
+ *  scale  max(amax, 2^-100) / 448 of the block, one IEEE FP32 division; code
+ *         E4M3_RNE(x / scale), the quotient rounded to FP32 first. A block with
+ *         a NaN or an infinity gets scale NaN and NaN codes.
+ * rows == 0 is a no-op. */
+nvfp4_status nvfp4_fp8_quantize(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, int gated,
+                                uint8_t *codes, float *scales, void *stream);
+
+/* The same for weights, a scale per 128 x 128 block: `experts` matrices [N][K]
+ * (1 for a single one), rows ldw and matrices expert_stride elements apart ->
+ * codes [experts][N][K], scales [experts][ceil(N/128)][ceil(K/128)]. The
+ * transposed weight of a gradient has the transposed codes and scales. */
+nvfp4_status nvfp4_fp8_quantize_weight(const void *w, int dtype, int64_t experts, int64_t N, int64_t K, int64_t ldw,
+                                       int64_t expert_stride, uint8_t *codes, float *scales, void *stream);
+
+/* out[m][n] = sum_b a_scales[m][b] w_scales[n/128][b] sum_{k in b} a[m][k] w[n][k],
+ * the outer sum in FP32, each inner one on the FP8 matrix core: of eight
+ * consecutive products of its order it keeps what is at least 2^-13 of their
+ * largest, and adds such sums in FP32.
+ *  out  [M][N] of dtype NVFP4_BF16 or NVFP4_F16 (rounded once), rows ldo
+ *       elements apart, 2-byte aligned.
+ *  M >= 0 (0 is a no-op), any N >= 1, K % 16 == 0.
+ *  ws   nvfp4_fp8_gemm_workspace_bytes(M, N, K) bytes on the current device,
+ *       16-byte aligned, not initialised; one per stream that runs
+ *       concurrently. May be NULL when that is 0. */
+size_t nvfp4_fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+nvfp4_status nvfp4_fp8_gemm(const uint8_t *a, const float *a_scales, const uint8_t *w, const float *w_scales, int64_t M,
+                            int64_t N, int64_t K, void *out, int dtype, int64_t ldo, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/* The same for rows sorted by expert: out rows offsets[e] .. offsets[e+1] - 1
+ * (of M; device int32 [experts + 1], ascending, as nvfp4_moe_sort gives them)
+ * are products with weight e of the stack w [experts][N][K].
+ *  rows  device int32 [M]: the row of a (of a_rows) that each row of out
+ *        multiplies, so that tokens need not be gathered; NULL: its own number
+ *        (a_rows >= M).
+ * Rows that no expert has, or whose entry of rows is not a row of a, are left
+ * as they were. Where the offsets do not ascend, what the rows of out get is
+ * not defined (nothing else is written). experts 1 .. 1024. */
+nvfp4_status nvfp4_fp8_gemm_grouped(const uint8_t *a, const float *a_scales, int64_t a_rows, const int32_t *rows,
+                                    const uint8_t *w, const float *w_scales, int32_t experts, const int32_t *offsets,
+                                    int64_t M, int64_t N, int64_t K, void *out, int dtype, int64_t ldo, void *stream);
+
+/* Sorts the (token, choice) pairs of a router by expert, pairs of one expert in
+ * the order of their number token * top + choice.
+ *  ids      device [tokens][top], int32 (id_bytes 4) or int64 (8): experts
+ *           0 .. experts - 1; any other id (-1: an expert of another device)
+ *           takes no part.
+ *  offsets  int32 out [experts + 1]: where each expert's pairs start; the last
+ *           entry is the number of pairs that take part.
+ *  sorted_tokens  int32 out [tokens * top]: the token of each sorted pair, -1
+ *           behind the last.
+ *  places   int32 out [tokens][top]: where each pair went, -1 for none.
+ *  experts 1 .. 1024, top >= 1, tokens * top < 2^31.
+ *  ws  nvfp4_moe_sort_workspace_bytes(...) bytes, 16-byte aligned, not initialised. */
+size_t nvfp4_moe_sort_workspace_bytes(int64_t tokens, int64_t top, int32_t experts);
+nvfp4_status nvfp4_moe_sort(const void *ids, int id_bytes, int64_t tokens, int64_t top, int32_t experts,
+                            int32_t *offsets, int32_t *sorted_tokens, int32_t *places, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/* Rows to their places and back. x [tokens][width], y [tokens * top][width] of
+ * dtype (any nvfp4_dtype), rows ld* elements apart, element-aligned; places as
+ * nvfp4_moe_sort gives them: the entries in range are distinct, one out of
+ * range (0 .. tokens * top - 1) stands for no row. Sums run over the choices in
+ * order, in FP32, and are rounded once. Outputs lie apart from inputs.
+ *  gather    out[places[t][j]] = x[t]; rows that no place names are left as
+ *            they were. Its gradient is combine without weights.
+ *  combine   out[t] = sum_j weights[t][j] y[places[t][j]] (weights device FP32
+ *            [tokens][top]; NULL: ones); zeros for a token without a row.
+ *  combine_backward  grad_y[places[t][j]] = weights[t][j] grad[t] (rows that no
+ *            place names are left as they were) and grad_weights[t][j] =
+ *            grad[t] . y[places[t][j]] (FP32, 0 for no row). */
+nvfp4_status nvfp4_moe_gather(const void *x, int dtype, int64_t ldx, const int32_t *places, int64_t tokens, int64_t top,
+                              int64_t width, void *out, int64_t ldo, void *stream);
+nvfp4_status nvfp4_moe_combine(const void *y, int dtype, int64_t ldy, const int32_t *places, const float *weights,
+                               int64_t tokens, int64_t top, int64_t width, void *out, int64_t ldo, void *stream);
+nvfp4_status nvfp4_moe_combine_backward(const void *grad, int64_t ldg, const void *y, int64_t ldy, int dtype,
+                                        const int32_t *places, const float *weights, int64_t tokens, int64_t top,
+                                        int64_t width, void *grad_y, int64_t ldo, float *grad_weights, void *stream);
 
 #ifdef __cplusplus
 }

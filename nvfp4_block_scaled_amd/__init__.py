@@ -14,6 +14,10 @@ Entry points (same names as the C ABI):
 and, on a key/value cache held in NVFP4 (kv_cache.py):
   nvfp4_kv_append, nvfp4_kv_read, nvfp4_kv_attention, nvfp4_kv_copy_pages, nvfp4_kv_fork, nvfp4_kv_resize,
   nvfp4_kv_compact
+in FP8 with block scales (fp8.py):
+  nvfp4_fp8_quantize, nvfp4_fp8_quantize_weight, nvfp4_fp8_gemm, nvfp4_fp8_gemm_grouped
+and between a router and its experts (moe.py):
+  nvfp4_moe_sort, nvfp4_moe_gather, nvfp4_moe_gather_backward, nvfp4_moe_combine, nvfp4_moe_combine_backward
 """
 import ctypes
 import os
@@ -120,6 +124,20 @@ _SIGS = [
      [_I64, _I32, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
     ("nvfp4_kv_compact", ctypes.c_int,
      [_P, _P, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("nvfp4_fp8_quantize", ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_int, _P, _P, _P]),
+    ("nvfp4_fp8_quantize_weight", ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _I64, _I64, _P, _P, _P]),
+    ("nvfp4_fp8_gemm_workspace_bytes", ctypes.c_size_t, [_I64, _I64, _I64]),
+    ("nvfp4_fp8_gemm", ctypes.c_int,
+     [_P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_int, _I64, _P, ctypes.c_size_t, _P]),
+    ("nvfp4_fp8_gemm_grouped", ctypes.c_int,
+     [_P, _P, _I64, _P, _P, _P, _I32, _P, _I64, _I64, _I64, _P, ctypes.c_int, _I64, _P]),
+    ("nvfp4_moe_sort_workspace_bytes", ctypes.c_size_t, [_I64, _I64, _I32]),
+    ("nvfp4_moe_sort", ctypes.c_int,
+     [_P, ctypes.c_int, _I64, _I64, _I32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("nvfp4_moe_gather", ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _I64, _I64, _I64, _P, _I64, _P]),
+    ("nvfp4_moe_combine", ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _P]),
+    ("nvfp4_moe_combine_backward", ctypes.c_int,
+     [_P, _I64, _P, _I64, ctypes.c_int, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _P]),
 ]
 EXPORTED = [s[0] for s in _SIGS]
 
@@ -576,3 +594,7 @@ def nvfp4_gemm_w4a4_two_pass_tiled(a2_tiled, M, w_prep, N, K, alpha=1.0, alpha_d
 from .kv_cache import (KVCache, nvfp4_kv_append, nvfp4_kv_attention, nvfp4_kv_attention_workspace,  # noqa: E402,F401
                        nvfp4_kv_compact, nvfp4_kv_copy_pages, nvfp4_kv_fork, nvfp4_kv_page_bytes, nvfp4_kv_read,
                        nvfp4_kv_resize)
+from .fp8 import (nvfp4_fp8_gemm, nvfp4_fp8_gemm_grouped, nvfp4_fp8_gemm_workspace, nvfp4_fp8_quantize,  # noqa: E402,F401
+                  nvfp4_fp8_quantize_weight)
+from .moe import (nvfp4_moe_combine, nvfp4_moe_combine_backward, nvfp4_moe_gather, nvfp4_moe_gather_backward,  # noqa: E402,F401
+                  nvfp4_moe_sort)

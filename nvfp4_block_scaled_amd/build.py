@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libnvfp4.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "config.hip", "quantize.hip", "gemm_w4a4.hip", "gemm_w4a16.hip",
-           "kv_append.hip", "kv_attention.hip", "kv_pages.hip"]
+           "kv_append.hip", "kv_attention.hip", "kv_pages.hip", "fp8_quantize.hip", "fp8_gemm.hip", "moe.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

@@ -1,0 +1,132 @@
+"""Tokens to experts and back: the Python entry points over the C ABI's nvfp4_moe_* (include/nvfp4.h).
+
+  offsets, tokens, places = nvfp4_moe_sort(ids, experts)          # ids [T][top]
+  rows = nvfp4_moe_gather(x, places)                              # [T * top][width], by expert
+  out = nvfp4_moe_combine(y, places, weights)                     # [T][width]
+
+and their gradients. Marshalling and checks only; everything is enqueued on the current stream and
+nothing synchronises. Ids and places lie in device memory and are checked there: one that is out of
+range stands for no row.
+"""
+import torch
+
+from . import _check, lib
+from .fp8 import _floats, _matrix, _rows_out
+from .kv_cache import _at, _bytes, _device, _flat, _stream
+
+_IDS = {torch.int32: 4, torch.int64: 8}
+
+
+def nvfp4_moe_sort(ids, experts, ws=None):
+    """Sorts (token, choice) pairs by expert: ids [T][top], int32 or int64, in 0 .. experts - 1 (any other,
+    like -1, takes no part). Returns (offsets int32 [experts + 1], tokens int32 [T * top], the token of each
+    sorted pair and -1 behind the last, places int32 [T][top], each pair's place or -1)."""
+    dev = _device()
+    _at(ids, "ids", dev)
+    if ids.dtype not in _IDS:
+        raise TypeError("ids must be int32 or int64")
+    if ids.dim() != 2 or ids.shape[1] < 1:
+        raise ValueError("ids must be [tokens][top]")
+    if not 1 <= experts <= 1024:
+        raise ValueError("experts must be 1 .. 1024")
+    ids = ids.contiguous()
+    T, top = ids.shape
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+    tokens = torch.empty(T * top, dtype=torch.int32, device=ids.device)
+    places = torch.empty((T, top), dtype=torch.int32, device=ids.device)
+    ws, wsp, nws = _bytes(ws, lib().nvfp4_moe_sort_workspace_bytes(T, top, experts), dev)
+    _check(lib().nvfp4_moe_sort(ids.data_ptr(), _IDS[ids.dtype], T, top, experts, offsets.data_ptr(), tokens.data_ptr(),
+                                places.data_ptr(), wsp, nws, _stream(dev)))
+    return offsets, tokens, places
+
+
+def _places(places, dev):
+    """(address, tokens, top)"""
+    if not isinstance(places, torch.Tensor) or places.dim() != 2 or places.shape[1] < 1:
+        raise TypeError("places must be a CUDA (HIP) tensor [tokens][top]")
+    return (_flat(places, "places", dev, torch.int32, tuple(places.shape)),) + tuple(places.shape)
+
+
+def _input(t, name, dev, rows):
+    kind = _floats(t, name, dev)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < 1:
+        raise ValueError(f"{name} must be [{rows}][>= 1], got {list(t.shape)}")
+    t, ld = _matrix(t, name)
+    return t, kind, ld
+
+
+def _apart(out, name, *inputs):
+    """An output must not share storage with an input in the bytes that both cover."""
+    lo, hi = out.data_ptr(), out.data_ptr() + _span(out)
+    for t in inputs:
+        if t.data_ptr() < hi and lo < t.data_ptr() + _span(t):
+            raise ValueError(f"{name} overlaps an input")
+
+
+def _span(t):
+    """Bytes from a matrix's first element to its last."""
+    if t.numel() == 0:
+        return 0
+    return ((t.shape[0] - 1) * t.stride(0) + (t.shape[1] - 1) * t.stride(1) + 1) * t.element_size()
+
+
+def _output(out, name, dev, rows, width, like, *inputs):
+    if out is None:
+        return torch.empty((rows, width), dtype=like.dtype, device=like.device), width
+    ld = _rows_out(out, name, dev, rows, width, like.dtype)
+    _apart(out, name, *inputs)
+    return out, ld
+
+
+def nvfp4_moe_gather(x, places, out=None):
+    """The tokens' rows x [T][width] (float32, bfloat16 or float16) in the order of their experts: row
+    places[t][j] of out [T * top][width] is x[t]. Rows that no place names are left as they were
+    (undefined in a new out)."""
+    dev = _device()
+    at, T, top = _places(places, dev)
+    x, kind, ldx = _input(x, "x", dev, T)
+    out, ldo = _output(out, "out", dev, T * top, x.shape[1], x, x)
+    _check(lib().nvfp4_moe_gather(x.data_ptr(), kind, ldx, at, T, top, x.shape[1], out.data_ptr(), ldo, _stream(dev)))
+    return out
+
+
+def _weights(weights, dev, T, top):
+    return _flat(weights, "weights", dev, torch.float32, (T, top))
+
+
+def nvfp4_moe_combine(y, places, weights=None, out=None):
+    """The sorted rows y [T * top][width] back to their tokens: out[t] = sum_j weights[t][j] y[places[t][j]]
+    (weights float32 [T][top]; None: ones), summed in FP32 in the order of j and rounded once."""
+    dev = _device()
+    at, T, top = _places(places, dev)
+    y, kind, ldy = _input(y, "y", dev, T * top)
+    w_at = None if weights is None else _weights(weights, dev, T, top)
+    out, ldo = _output(out, "out", dev, T, y.shape[1], y, y)
+    _check(lib().nvfp4_moe_combine(y.data_ptr(), kind, ldy, at, w_at, T, top, y.shape[1], out.data_ptr(), ldo,
+                                   _stream(dev)))
+    return out
+
+
+def nvfp4_moe_gather_backward(grad, places, out=None):
+    """The gradient of nvfp4_moe_gather's x from that of its rows, grad [T * top][width]: each token's rows added."""
+    return nvfp4_moe_combine(grad, places, None, out)
+
+
+def nvfp4_moe_combine_backward(grad, y, places, weights, grad_y=None):
+    """The gradients of nvfp4_moe_combine's y and weights from its out's, grad [T][width]: (grad_y
+    [T * top][width] with row places[t][j] = weights[t][j] grad[t], grad_weights float32 [T][top]). Rows
+    of grad_y that no place names are left as they were (undefined in a new grad_y)."""
+    dev = _device()
+    at, T, top = _places(places, dev)
+    y, kind, ldy = _input(y, "y", dev, T * top)
+    grad, other, ldg = _input(grad, "grad", dev, T)
+    if other != kind:
+        raise TypeError("grad and y must have one type")
+    if grad.shape[1] != y.shape[1]:
+        raise ValueError(f"grad has {grad.shape[1]} columns, y {y.shape[1]}")
+    w_at = _weights(weights, dev, T, top)
+    grad_y, ldo = _output(grad_y, "grad_y", dev, T * top, y.shape[1], y, y, grad)
+    grad_weights = torch.empty((T, top), dtype=torch.float32, device=y.device)
+    _check(lib().nvfp4_moe_combine_backward(grad.data_ptr(), ldg, y.data_ptr(), ldy, kind, at, w_at, T, top, y.shape[1],
+                                            grad_y.data_ptr(), ldo, grad_weights.data_ptr(), _stream(dev)))
+    return grad_y, grad_weights
