@@ -12,13 +12,24 @@
 // in FP32; measured on gaussian rows that is 1.3e-5 of the result, a hundredth
 // of the rounding to BF16, which is why no FP32 output is offered). W is the
 // instruction's first operand, so a lane holds four consecutive columns of one
-// row: one scale a lane, and 8-byte stores.
+// row: one scale a lane.
 //
 // Order of K inside a block: lane group g = lane / 16 has the 16-byte units g
 // and g + 4 of its row. A and W use the same order, so each product is met once.
+//
+// tile_kernel does the work (operands through LDS, workgroups that walk several
+// tiles); stream_kernel, with operands straight into registers and 64-bit
+// addresses, what it does not take.
+#include <math.h>
+
+#include <algorithm>
+
 #include "common.hpp"
 
 namespace nvfp4 {
+
+int device_cus_or_default();
+
 namespace fp8 {
 
 typedef int v8i_t __attribute__((ext_vector_type(8)));
@@ -36,35 +47,47 @@ struct GemmArgs {
   const int32_t *rows;        // row of A of each sorted row, or null: its own number
   int64_t a_rows;             // rows of A
   int32_t experts;
+  // K in parts
+  int32_t parts;
+  float *partial;             // [parts][M][N rounded up to 4]
 };
 
-// 64 lanes x 16 bytes (or 4) from global memory to consecutive bytes of LDS,
-// with no register between. The compiler does not see the load: every reader
-// waits for vmcnt and passes a barrier first.
-__device__ __forceinline__ void to_lds16(const uint8_t *src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "m0", "memory");
+// Loads of 64 lanes x 16 (or 4) bytes to consecutive bytes of LDS, with no
+// register between, from a buffer whose end the hardware checks: past it, zeros
+// arrive. The compiler does not see these loads: every reader waits for vmcnt
+// and passes a barrier first.
+__device__ __forceinline__ void to_lds16(u32x4_t buf, uint32_t off, uint32_t lds, int plus) {
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(buf), "i"(plus)
+               : "m0", "scc", "memory");
 }
-__device__ __forceinline__ void to_lds4(const float *src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "m0", "memory");
+// Only when `skip` is 0 (a branch that the compiler does not see: one of its
+// own would part the step that it schedules as a whole).
+__device__ __forceinline__ void to_lds4_if(u32x4_t buf, uint32_t off, uint32_t lds, uint32_t skip) {
+  asm volatile(
+      "s_cmp_lg_u32 %3, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\t"
+      "buffer_load_dword %1, %2, 0 offen lds\n.Lskip%=:" ::"s"(lds),
+      "v"(off), "s"(buf), "s"(skip)
+      : "m0", "scc", "memory");
 }
+// A buffer of the bytes base + from .. base + size - 1 (from <= size).
+__device__ __forceinline__ u32x4_t buffer(const void *base, uint32_t size, uint32_t from) {
+  const uint64_t at = (uint64_t)(uintptr_t)base + from;
+  return u32x4_t{(uint32_t)at, (uint32_t)(at >> 32), size - from, 0x00020000u};
+}
+__device__ __forceinline__ uint32_t bytes32(int64_t n) { return (uint32_t)min(n, (int64_t)0xFFFFFFE0); }
+constexpr uint32_t kPastEnd = 0xFFFFFFF0u;      // an offset past the end of any such buffer
 
 __device__ __forceinline__ v8i_t join(u32x4_t a, u32x4_t b) {
   return v8i_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
-// The tile of a workgroup: rows [m0, m1) of out against columns from n0 of the
-// weight `expert`. Workgroups of one XCD (ids congruent mod 8) get consecutive
-// tiles, so that what they share meets in that XCD's L2.
+// Rows m0 .. m1 - 1 of out (as many of them as a tile has) against columns from
+// n0 of the weight `expert`, over all blocks of K or a part of them.
 struct Tile {
   int64_t m0, m1, n0;
   int32_t expert;
+  int32_t k0, blocks, part;   // blocks of K from k0 on; the part of K that they are
 };
-
-__device__ __forceinline__ bool xcd_order(uint32_t b, uint32_t total, uint32_t *t) {
-  const uint32_t per = (total + 7) / 8;
-  *t = (b & 7) * per + (b >> 3);
-  return (b >> 3) < per && *t < total;
-}
 
 constexpr int kBand = 8;     // tile rows of a band: within one, tiles go down the columns
 
@@ -75,244 +98,676 @@ __device__ __forceinline__ void band_order(uint32_t t, uint32_t rows, uint32_t c
   *n = w / tall;
 }
 
-// The workgroup's tile among those of the experts that have rows, expert by
-// expert; every workgroup counts them all (the host does not know the rows).
-// Offsets are taken within 0 .. M, an end below its start as no rows.
+// Tiles of experts that have rows, expert by expert: the host does not know the
+// rows, so every workgroup counts the tiles itself, into LDS, and finds its own
+// by the counts. Offsets are taken within 0 .. M, an end below its start as no rows.
+constexpr int kMaxExperts = 1024;
+
+__device__ __forceinline__ void expert_rows(const GemmArgs &a, int e, int32_t *lo, int32_t *hi) {
+  *lo = max(0, min(a.offsets[e], (int32_t)a.M));
+  *hi = max(*lo, min(a.offsets[e + 1], (int32_t)a.M));
+}
+
+// upto[e]: tiles of BM rows of the experts 0 .. e; returns those of all.
 template <int BM, int THREADS>
-__device__ __forceinline__ bool grouped_tile(const GemmArgs &a, uint32_t b, int32_t *sh, Tile *tile) {
-  // sh[0 .. WAVES): sums of waves; then the answer
-  constexpr int WAVES = THREADS / 64;
+__device__ __forceinline__ uint32_t count_tiles(const GemmArgs &a, uint32_t *upto, uint32_t *sums) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  uint32_t total = 0;
-  if (tid == 0) sh[WAVES] = -1;
-  for (int pass = 0; pass < 2; pass++) {
-    uint32_t t = 0;
-    if (pass == 1 && !xcd_order(b, total * (uint32_t)a.tiles_n, &t)) return false;
-    uint32_t base = 0;                           // m tiles of the experts before this round's
-    for (int e0 = 0; e0 < a.experts; e0 += THREADS) {
-      const int e = e0 + tid;
-      int32_t lo = 0, hi = 0;
-      if (e < a.experts) {
-        lo = max(0, min(a.offsets[e], (int32_t)a.M));
-        hi = max(lo, min(a.offsets[e + 1], (int32_t)a.M));
-      }
-      const uint32_t mine = ((uint32_t)(hi - lo) + BM - 1) / BM;
-      uint32_t run = mine;
+  uint32_t base = 0;
+  for (int e0 = 0; e0 < a.experts; e0 += THREADS) {
+    const int e = e0 + tid;
+    int32_t lo = 0, hi = 0;
+    if (e < a.experts) expert_rows(a, e, &lo, &hi);
+    uint32_t run = ((uint32_t)(hi - lo) + BM - 1) / BM;
 #pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const uint32_t v = __shfl_up(run, d);
-        if (lane >= d) run += v;
-      }
-      __syncthreads();
-      if (lane == 63) sh[wave] = (int32_t)run;
-      __syncthreads();
-      uint32_t before = base + run - mine;
-#pragma unroll
-      for (int w = 0; w < WAVES; w++) {
-        if (w < wave) before += (uint32_t)sh[w];
-        base += (uint32_t)sh[w];
-      }
-      if (pass == 1 && mine > 0 && t >= before * (uint32_t)a.tiles_n && t < (before + mine) * (uint32_t)a.tiles_n) {
-        const uint32_t w = t - before * (uint32_t)a.tiles_n;       // within the expert: down the rows, then across
-        sh[WAVES] = e;
-        sh[WAVES + 1] = lo + (int32_t)(w % mine) * BM;
-        sh[WAVES + 2] = hi;
-        sh[WAVES + 3] = (int32_t)(w / mine);
-      }
+    for (int d = 1; d < 64; d *= 2) {
+      const uint32_t v = __shfl_up(run, d);
+      if (lane >= d) run += v;
     }
-    if (pass == 0) total = base;
+    if (lane == 63) sums[wave] = run;
+    __syncthreads();
+    for (int w = 0; w < THREADS / 64; w++) {
+      if (w < wave) run += sums[w];
+    }
+    if (e < a.experts) upto[e] = base + run;
+    for (int w = 0; w < THREADS / 64; w++) base += sums[w];
+    __syncthreads();
   }
-  __syncthreads();
-  tile->expert = __builtin_amdgcn_readfirstlane(sh[WAVES]);
-  if (tile->expert < 0) return false;
-  tile->m0 = __builtin_amdgcn_readfirstlane(sh[WAVES + 1]);
-  tile->m1 = __builtin_amdgcn_readfirstlane(sh[WAVES + 2]);
-  tile->n0 = __builtin_amdgcn_readfirstlane(sh[WAVES + 3]);
+  return base;
+}
+
+// Tile t, down the rows of an expert, then across its columns.
+template <int BM, int BN>
+__device__ __forceinline__ bool find_tile(const GemmArgs &a, const uint32_t *upto, uint32_t t, Tile *tile) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t q = t / (uint32_t)a.tiles_n;
+  int e = 0;
+  for (int e0 = 0; e0 < a.experts; e0 += 64) e += __popcll(__ballot(e0 + lane < a.experts && upto[min(e0 + lane, a.experts - 1)] <= q));
+  if (e >= a.experts) return false;
+  int32_t lo, hi;
+  expert_rows(a, e, &lo, &hi);
+  const uint32_t mine = ((uint32_t)(hi - lo) + BM - 1) / BM;
+  const uint32_t w = t - (upto[e] - mine) * (uint32_t)a.tiles_n;
+  if (mine == 0 || w / mine >= (uint32_t)a.tiles_n) return false;      // only where the offsets do not ascend
+  tile->expert = __builtin_amdgcn_readfirstlane(e);
+  tile->m0 = __builtin_amdgcn_readfirstlane(lo + (int32_t)(w % mine) * BM);
+  tile->m1 = __builtin_amdgcn_readfirstlane(hi);
+  tile->n0 = (int64_t)__builtin_amdgcn_readfirstlane(w / mine) * BN;
   return true;
 }
 
-// WM x WN waves share a BM x BN tile; a wave has TM x TN tiles of 16 x 16.
-// STAGES blocks of K lie in LDS at a time, rows of 128 bytes whose 16-byte
-// units are exchanged by the low bits of the row (unit u of row r lies at
-// u ^ (r & 7)), so that neither the loads nor the fragments' reads meet in a bank.
-template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, bool F16>
+// The row of A that row m of out multiplies (one of A's in any case: what a row
+// without one gives is not stored).
+template <bool GROUPED>
+__device__ __forceinline__ int64_t row_of_a(const GemmArgs &p, const Tile &t, int64_t m) {
+  m = min(m, t.m1 - 1);
+  if (GROUPED && p.rows) {
+    const int64_t at = p.rows[m];
+    return at < 0 || at >= p.a_rows ? 0 : at;
+  }
+  return m;
+}
+
+template <bool GROUPED>
+__device__ __forceinline__ bool row_is_stored(const GemmArgs &p, const Tile &t, int64_t m) {
+  if (m >= t.m1) return false;
+  return !GROUPED || !p.rows || (p.rows[m] >= 0 && p.rows[m] < p.a_rows);
+}
+
+// Two FP32 values rounded to the output's type.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if (F16) {
+    const half2_t v = {(_Float16)a, (_Float16)b};
+    uint32_t u;
+    __builtin_memcpy(&u, &v, 4);
+    return u;
+  }
+  return (uint32_t)f32_to_bf16_rne(a) | ((uint32_t)f32_to_bf16_rne(b) << 16);
+}
+
+// BM x BN tiles, WM x WN waves of TM x TN matrix tiles each. STAGES blocks of K
+// lie in LDS, rows of 128 bytes whose 16-byte units are exchanged by the low
+// bits of the row (unit u of row r lies at u ^ (r & 7)), so that neither the
+// loads nor the fragments' reads meet in a bank. A workgroup walks several
+// tiles, and its loads run STAGES blocks ahead, across the end of a tile into
+// the next one, so nothing starts cold but the first.
+//
+// A step is one block: TM times (the next rows' fragment is read, TN products,
+// the sums of the rows before). Before the last rows' products the wave waits:
+// the next block has arrived and everybody has read this one, whose place the
+// loads of a later block take; the next block's fragments are read among the
+// last products. Eight waves of 128 x 64 leave 512 / 2 registers a lane: 128
+// sums, 48 of fragments, 32 of products under way.
+template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, bool SPLIT, bool F16>
 __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(GemmArgs p) {
   constexpr int WAVES = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
-  constexpr int SCALES = BM < 64 ? 256 : BM * 4;            // a wave's load brings 64 scales
-  constexpr int STAGE = (BM + BN) * 128 + SCALES;
-  constexpr int LOADS_A = BM / 8 / WAVES, LOADS_W = BN / 8 / WAVES;
-  static_assert(LOADS_A * 8 * WAVES == BM && LOADS_W * 8 * WAVES == BN, "whole loads for every wave");
-  static_assert(BN / WN <= 128 && 128 % (BN / WN) == 0, "a wave's columns have one scale");
-  static_assert(STAGES == 2, "the wait at the top of a step is for everything in flight");
-  __shared__ __attribute__((aligned(128))) uint8_t lds[STAGES * STAGE];
-  __shared__ int32_t found[WAVES + 4];
+  constexpr int LA = BM / 8 / WAVES, LW = BN / 8 / WAVES;                 // loads of a wave for a block
+  constexpr int CHUNKS = BM / 16, LS = (CHUNKS + WAVES - 1) / WAVES;      // 16 rows' scales to a load (by two waves, where few)
+  constexpr int CB = (BN + 127) / 128;
+  constexpr int STAGE = (BM + BN) * 128, SCALES = BM * 16, COLS = CB * 256, OUT = 16 * TN * 32;
+  static_assert(LA * 8 * WAVES == BM && LW * 8 * WAVES == BN, "whole loads for every wave");
+  static_assert(128 % (BN / WN) == 0 && TM % 2 == 0 && (STAGES & (STAGES - 1)) == 0 && STAGES >= 2, "");
+  __shared__ __attribute__((aligned(128))) uint8_t lds[STAGES * (STAGE + SCALES + COLS) + WAVES * OUT];
+  __shared__ uint32_t upto[GROUPED ? kMaxExperts : 1], sums[WAVES];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4, wm = wave / WN, wn = wave % WN;
+  const int blocks = p.blocks;
 
-  Tile t;
-  if constexpr (GROUPED) {
-    if (!grouped_tile<BM, 64 * WAVES>(p, blockIdx.x, found, &t)) return;
-    t.n0 *= BN;
-  } else {
-    uint32_t id, tm, tn;
-    if (!xcd_order(blockIdx.x, (uint32_t)p.tiles_m * (uint32_t)p.tiles_n, &id)) return;
-    band_order(id, p.tiles_m, p.tiles_n, &tm, &tn);
-    t.m0 = (int64_t)tm * BM;
-    t.m1 = p.M;
-    t.n0 = (int64_t)tn * BN;
-    t.expert = 0;
-  }
-
-  // The row of A that row m of out multiplies (clamped into A: what it gives is not stored).
-  auto a_row = [&](int64_t m) -> int64_t {
-    m = min(m, t.m1 - 1);
-    if (GROUPED && p.rows) {
-      const int64_t at = p.rows[m];
-      return at < 0 || at >= p.a_rows ? 0 : at;
+  uint32_t total = (uint32_t)p.tiles_m * (uint32_t)p.tiles_n * (SPLIT ? (uint32_t)p.parts : 1u);
+  if constexpr (GROUPED)
+    total = __builtin_amdgcn_readfirstlane(count_tiles<BM, 64 * WAVES>(p, upto, sums)) * (uint32_t)p.tiles_n;
+  // Workgroups of one XCD (ids congruent mod 8) walk one eighth of the tiles side by side, so that what neighbours
+  // share meets in that XCD's L2.
+  const uint32_t per = (total + 7) / 8, stride = gridDim.x / 8;
+  uint32_t at = blockIdx.x / 8;
+  const uint32_t first = (blockIdx.x & 7) * per;
+  auto tile_at = [&](uint32_t i, Tile *t) {
+    if (i >= per || first + i >= total) return false;
+    t->k0 = t->part = 0;
+    t->blocks = blocks;
+    if constexpr (GROUPED) {
+      return find_tile<BM, BN>(p, upto, first + i, t);
+    } else {
+      uint32_t id = first + i, tm, tn;
+      if constexpr (SPLIT) {       // parts lie side by side in the order: the first `blocks % parts` have a block more
+        const uint32_t q = id % (uint32_t)p.parts, each = (uint32_t)blocks / (uint32_t)p.parts, more = (uint32_t)blocks % (uint32_t)p.parts;
+        id /= (uint32_t)p.parts;
+        t->part = (int32_t)q;
+        t->k0 = (int32_t)(q * each + min(q, more));
+        t->blocks = (int32_t)(each + (q < more));
+      }
+      band_order(id, p.tiles_m, p.tiles_n, &tm, &tn);
+      t->m0 = (int64_t)tm * BM;
+      t->m1 = p.M;
+      t->n0 = (int64_t)tn * BN;
+      t->expert = 0;
+      return true;
     }
+  };
+
+  // What loads need of a tile: where its rows and columns begin and how many bytes follow. Lanes' offsets from
+  // there are the same for every tile, or, of rows taken through an index, the index's. A load brings eight rows.
+  struct Aim {
+    const uint8_t *a, *w, *s, *c;
+    uint32_t a_left, w_left, s_left, c_left;      // bytes
+    uint32_t last_at;                             // where a row's last 128 bytes begin
+    int32_t last;                                 // the row's last block
+  };
+  const bool indexed = GROUPED && p.rows;
+  const int unit = ((lane & 7) ^ ((lane >> 3) & 7)) * 16;
+  uint32_t off_a[LA], off_w[LW], off_s[LS];
+#pragma unroll
+  for (int i = 0; i < LA; i++) off_a[i] = (uint32_t)(((wave * LA + i) * 8 + (lane >> 3)) * p.K + unit);
+#pragma unroll
+  for (int i = 0; i < LW; i++) off_w[i] = (uint32_t)(((wave * LW + i) * 8 + (lane >> 3)) * p.K + unit);
+#pragma unroll
+  for (int i = 0; i < LS; i++) off_s[i] = (uint32_t)(((wave * LS + i) % CHUNKS * 16 + (lane >> 2)) * blocks + (lane & 3)) * 4;
+  auto index_rows = [&](const Tile &t) {
+    if (indexed) {
+#pragma unroll
+      for (int i = 0; i < LA; i++)
+        off_a[i] = (uint32_t)(row_of_a<GROUPED>(p, t, t.m0 + (wave * LA + i) * 8 + (lane >> 3)) * p.K + unit);
+#pragma unroll
+      for (int i = 0; i < LS; i++)
+        off_s[i] = (uint32_t)(row_of_a<GROUPED>(p, t, t.m0 + (wave * LS + i) % CHUNKS * 16 + (lane >> 2)) * blocks + (lane & 3)) * 4;
+    }
+  };
+  auto aim = [&](const Tile &t) {
+    const int64_t first_row = indexed ? 0 : t.m0, rows = indexed ? p.a_rows : GROUPED ? p.a_rows : p.M;
+    const int64_t cb = (p.N + 127) / 128, c0 = min(t.n0 / 128 + wave % CB, cb - 1);
+    Aim m;
+    const int64_t skip = SPLIT ? t.k0 : 0;
+    m.a = p.a + first_row * p.K + skip * 128;
+    m.a_left = bytes32((rows - first_row) * p.K - skip * 128);
+    m.s = reinterpret_cast<const uint8_t *>(p.a_scales + first_row * blocks + skip);
+    m.s_left = bytes32(((rows - first_row) * blocks - skip) * 4);
+    m.w = p.w + ((int64_t)t.expert * p.N + t.n0) * p.K + skip * 128;
+    m.w_left = bytes32((p.N - t.n0) * p.K - skip * 128);
+    m.c = reinterpret_cast<const uint8_t *>(p.w_scales + ((int64_t)t.expert * cb + c0) * blocks + skip);
+    m.c_left = bytes32(((cb - c0) * blocks - skip) * 4);
+    m.last_at = (uint32_t)(p.K - 128 - skip * 128);
+    m.last = blocks - 1 - (int32_t)skip;
     return m;
   };
 
-  // Addresses of this lane's part of each load: row lane / 8 of eight, unit
-  // (lane % 8) ^ (row % 8) of its 128 bytes.
-  const int unit = ((lane & 7) ^ ((lane >> 3) & 7)) * 16;
-  const uint8_t *src[LOADS_A + LOADS_W];
-#pragma unroll
-  for (int i = 0; i < LOADS_A; i++) src[i] = p.a + a_row(t.m0 + (wave * LOADS_A + i) * 8 + (lane >> 3)) * p.K + unit;
-  const int64_t w_base = (int64_t)t.expert * p.N;
-#pragma unroll
-  for (int i = 0; i < LOADS_W; i++) {
-    const int64_t n = min(t.n0 + (wave * LOADS_W + i) * 8 + (lane >> 3), p.N - 1);
-    src[LOADS_A + i] = p.w + (w_base + n) * p.K + unit;
-  }
-  constexpr int SCALE_CHUNKS = (BM + 63) / 64;
-  const int chunk = wave % SCALE_CHUNKS;                    // waves beyond the chunks bring the same values again
-  const float *src_s = p.a_scales + a_row(t.m0 + min(chunk * 64 + lane, BM - 1)) * p.blocks;
-  const float *sw = p.w_scales + ((int64_t)t.expert * ((p.N + 127) / 128) + min(t.n0 + wn * (BN / WN), p.N - 1) / 128) * p.blocks;
-
   const uint32_t base = (uint32_t)(uintptr_t)(lds_u8 *)lds;
-  auto load = [&](int kb) {
-    const uint32_t at = base + (kb & 1) * STAGE;
-    const int64_t k0 = (int64_t)kb * 128;
-    // units past the end of a row: its last unit in their place (masked below)
-    const int over = (int)max((int64_t)0, k0 + unit + 16 - p.K);
-    const int64_t off = k0 - over;
+  constexpr int AT_S = STAGES * STAGE, AT_C = AT_S + STAGES * SCALES;      // as many places for scales: a tile's last ones and the next's meet
+  // The last block is read from K - 128 on: units of it that the block before it had come as zeros (of A: a code of W
+  // that is not a number has met its row's product already).
+  const int from = (blocks * 8 - (int)(p.K / 16)) * 16;
+  // Block kb of a tile to the place of block vb in the order of all tiles; gb and cb count groups of four and of 64 in
+  // that order.
+  auto load = [&](const Aim &m, int kb, uint32_t vb, uint32_t gb, uint32_t cb) {
+    const uint32_t k0 = min((uint32_t)kb * 128, m.last_at);
+    const uint32_t to = base + (vb & (STAGES - 1)) * STAGE;
+    const u32x4_t bw = buffer(m.w, m.w_left, k0), ba = buffer(m.a, m.a_left, k0);
 #pragma unroll
-    for (int i = 0; i < LOADS_A; i++) to_lds16(src[i] + off, at + (wave * LOADS_A + i) * 1024);
+    for (int i = 0; i < LW; i++) to_lds16(bw, off_w[i], to + wave * LW * 1024, BM * 128 + i * 1024);
+    const bool had = kb == m.last && unit < from;
 #pragma unroll
-    for (int i = 0; i < LOADS_W; i++) to_lds16(src[LOADS_A + i] + off, at + BM * 128 + (wave * LOADS_W + i) * 1024);
-    to_lds4(src_s + kb, at + (BM + BN) * 128 + chunk * 256);
+    for (int i = 0; i < LA; i++) to_lds16(ba, had ? kPastEnd : off_a[i], to + wave * LA * 1024, i * 1024);
+    const u32x4_t bs = buffer(m.s, m.s_left, (uint32_t)kb * 4);
+#pragma unroll
+    for (int i = 0; i < LS; i++)       // with every fourth block, the rows' scales of four: [row][4]
+      to_lds4_if(bs, off_s[i], base + AT_S + (gb & (STAGES - 1)) * SCALES + (wave * LS + i) % CHUNKS * 256, kb & 3);
+    // with every 64th, the columns' scales of 64, by a wave for each 128 columns
+    to_lds4_if(buffer(m.c, m.c_left, (uint32_t)kb * 4), (uint32_t)lane * 4, base + AT_C + (cb & (STAGES - 1)) * COLS + wave % CB * 256,
+               (kb & 63) | (wave / CB));
+  };
+  auto arrived = [] {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"((STAGES - 2) * (LA + LW)) : "memory");
+  };
+
+  const uint32_t lo = (uint32_t)(r * 128 + ((g ^ (r & 7)) * 16)), hi = lo ^ 64;
+  auto fragment = [&](const uint8_t *at) {
+    return join(*reinterpret_cast<const u32x4_t *>(at + lo), *reinterpret_cast<const u32x4_t *>(at + hi));
+  };
+  auto rows_at = [&](uint32_t vb) { return lds + (vb & (STAGES - 1)) * STAGE + wm * (BM / WM) * 128; };
+  auto cols_at = [&](uint32_t vb) { return lds + (vb & (STAGES - 1)) * STAGE + BM * 128 + wn * (BN / WN) * 128; };
+  auto scales_at = [&](uint32_t gb, uint32_t k4) {
+    return reinterpret_cast<const float *>(lds + AT_S + (gb & (STAGES - 1)) * SCALES) + (wm * (BM / WM) + r) * 4 + k4;
+  };
+  auto col_at = [&](uint32_t cb, uint32_t k64) {
+    return reinterpret_cast<const float *>(lds + AT_C + (cb & (STAGES - 1)) * COLS) + wn * (BN / WN) / 128 * 64 + k64;
   };
 
   f32x4_t acc[TM][TN];
+  v8i_t w[TN], x[2];
+  float raw[TM], sa[TM], col;
+  // Block vb, whose first fragments and scales are in w, x[0], raw[0] and col; sc: its rows' scales; then the same of the
+  // block after it (next_sc, next_col). issue() loads the block that takes this one's place.
+  auto block = [&](uint32_t vb, const float *sc, const float *next_sc, const float *next_col, auto issue) {
+    const uint8_t *fa = rows_at(vb);
+    const float s = col;
+    f32x4_t d[2][TN];
 #pragma unroll
-  for (int i = 0; i < TM; i++)
-#pragma unroll
-    for (int j = 0; j < TN; j++) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-
-  const uint32_t lo = (uint32_t)(r * 128 + ((g ^ (r & 7)) * 16)), hi = lo ^ 64;
-  auto step = [&](int kb, float s, int valid) {           // valid: 16-byte units of the block
-    const uint8_t *st = lds + (kb & 1) * STAGE;
-    const uint8_t *fa = st + wm * (BM / WM) * 128, *fw = st + BM * 128 + wn * (BN / WN) * 128;
-    const float *sc = reinterpret_cast<const float *>(st + (BM + BN) * 128) + wm * (BM / WM);
-    auto fragment = [&](const uint8_t *at) {
-      u32x4_t x = *reinterpret_cast<const u32x4_t *>(at + lo), y = *reinterpret_cast<const u32x4_t *>(at + hi);
-      if (valid < 8) {
-        const u32x4_t z = {0u, 0u, 0u, 0u};
-        if (g >= valid) x = z;
-        if (g + 4 >= valid) y = z;
+    for (int i = 0; i <= TM; i++) {
+      if (i < TM) sa[i] = raw[i] * s;
+      if (i + 1 < TM) {
+        x[(i + 1) & 1] = fragment(fa + (i + 1) * 2048);
+        raw[i + 1] = sc[(i + 1) * 64];
       }
-      return join(x, y);
-    };
-    v8i_t w[TN];
-#pragma unroll
-    for (int j = 0; j < TN; j++) w[j] = fragment(fw + j * 2048);
-#pragma unroll
-    for (int i = 0; i < TM; i++) {
-      const v8i_t x = fragment(fa + i * 2048);
-      const float sa = sc[i * 16 + r] * s;
-#pragma unroll
-      for (int j = 0; j < TN; j++) {
-        const f32x4_t d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[j], x, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0,
-                                                                          0, 0, 0);
-#pragma unroll
-        for (int q = 0; q < 4; q++) acc[i][j][q] = __builtin_fmaf(sa, d[q], acc[i][j][q]);
+      if (i == TM - 1) {
+        arrived();
+        issue();
+        x[0] = fragment(rows_at(vb + 1));
+        raw[0] = *next_sc;
+        col = *next_col;
       }
+      if (i < TM) {
+#pragma unroll
+        for (int j = 0; j < TN; j++) {
+          d[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[j], x[i & 1], f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+          if (i == TM - 1) {
+            __builtin_amdgcn_sched_barrier(0);
+            w[j] = fragment(cols_at(vb + 1) + j * 2048);
+          }
+        }
+      }
+      if (i > 0) {
+#pragma unroll
+        for (int j = 0; j < TN; j++)
+#pragma unroll
+          for (int q = 0; q < 4; q++) acc[i - 1][j][q] = __builtin_fmaf(sa[i - 1], d[(i - 1) & 1][j][q], acc[i - 1][j][q]);
+      }
+      if (i < TM - 1) {      // reads first, then a product and four sums in turn
+        __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+#pragma unroll
+        for (int j = 0; j < TN; j++) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  load(0);
-  for (int kb = 0; kb < p.blocks; kb++) {
-    const float s = sw[kb];
-    // everything in flight has arrived and, past the barrier, everybody's; nobody reads the other stage any more
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (kb + 1 < p.blocks) load(kb + 1);
-    const int64_t left = p.K - (int64_t)kb * 128;
-    if (left >= 128) step(kb, s, 8);
-    else step(kb, s, (int)(left / 16));
-  }
-
-  // Lane (r, g) has columns 4 g .. 4 g + 3 of row r of each 16 x 16 tile.
-  typedef u32x2_t U __attribute__((aligned(2)));
+  Tile t;
+  if (!tile_at(at, &t)) return;
+  Aim here = aim(t);
+  index_rows(t);
+  uint32_t v = 0, gr = 0, ch = 0;        // blocks, groups of four and of 64 that came before the tile
 #pragma unroll
-  for (int i = 0; i < TM; i++) {
-    const int64_t m = t.m0 + wm * (BM / WM) + i * 16 + r;
-    bool stored = m < t.m1;
-    if (GROUPED && p.rows && stored) stored = p.rows[m] >= 0 && p.rows[m] < p.a_rows;
-    if (!stored) continue;
-    uint16_t *row = static_cast<uint16_t *>(p.out) + m * p.ldo;
+  for (int b = 0; b < STAGES; b++) load(here, b, b, b >> 2, 0);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"((STAGES - 1) * (LA + LW)) : "memory");
+  x[0] = fragment(rows_at(0));
 #pragma unroll
-    for (int j = 0; j < TN; j++) {
-      const int64_t n = t.n0 + wn * (BN / WN) + j * 16 + g * 4;
-      uint16_t h[4];
+  for (int j = 0; j < TN; j++) w[j] = fragment(cols_at(0) + j * 2048);
+  raw[0] = *scales_at(0, 0);
+  col = *col_at(0, 0);
+  for (;;) {
+    Tile next = t;
+    const bool more = tile_at(at + stride, &next);      // without one, the loads bring what nobody reads
+    const Aim then = aim(next);
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        if (F16) {
-          const _Float16 v = (_Float16)acc[i][j][q];
-          __builtin_memcpy(&h[q], &v, 2);
-        } else {
-          h[q] = f32_to_bf16_rne(acc[i][j][q]);
+    for (int i = 0; i < TM; i++)
+#pragma unroll
+      for (int j = 0; j < TN; j++) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const int nb = SPLIT ? t.blocks : blocks;
+    const uint32_t ng = gr + (nb + 3) / 4, nc = ch + (nb + 63) / 64;
+    for (int kb = 0; kb < nb - STAGES; kb++) {
+      const int kn = kb + 1, kl = kb + STAGES;
+      block(v + kb, scales_at(gr + (kb >> 2), kb & 3), scales_at(gr + (kn >> 2), kn & 3), col_at(ch + (kn >> 6), kn & 63),
+            [&] { load(here, kl, v + kl, gr + (kl >> 2), ch + (kl >> 6)); });
+    }
+    index_rows(next);
+    for (int kb = nb - STAGES; kb < nb; kb++) {
+      const bool end = kb + 1 == nb;
+      const int kn = end ? 0 : kb + 1, kl = kb + STAGES - nb;
+      block(v + kb, scales_at(gr + (kb >> 2), kb & 3), scales_at((end ? ng : gr) + (kn >> 2), kn & 3),
+            col_at((end ? nc : ch) + (kn >> 6), kn & 63), [&] { load(then, kl, v + nb + kl, ng + (kl >> 2), nc + (kl >> 6)); });
+    }
+    if constexpr (SPLIT) {      // FP32 sums of this part of K: [part][M][N rounded up to 4]
+      const int64_t ld = (p.N + 3) / 4 * 4;
+#pragma unroll
+      for (int i = 0; i < TM; i++) {
+        const int64_t m = t.m0 + wm * (BM / WM) + i * 16 + r;
+        float *row = p.partial + ((int64_t)t.part * p.M + m) * ld;
+#pragma unroll
+        for (int j = 0; j < TN; j++) {
+          const int64_t n = t.n0 + wn * (BN / WN) + j * 16 + g * 4;
+          if (m < p.M && n < ld) *reinterpret_cast<f32x4_t *>(row + n) = acc[i][j];
         }
       }
-      if (n + 4 <= p.N) {
-        const u32x2_t v = {(uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16)};
-        *reinterpret_cast<U *>(row + n) = v;
-      } else {
+    } else {
+      // The wave's results leave through LDS of its own, 16 rows at a time, in whole lines (TN = 4: 128 bytes a row).
+      constexpr int UNITS = TN * 2, ROWS = 64 / UNITS < 16 ? 64 / UNITS : 16;
+      uint8_t *mine = lds + AT_C + STAGES * COLS + wave * OUT;
+      const int row = lane / UNITS % ROWS, u8 = lane % UNITS;
+      const int64_t n = t.n0 + wn * (BN / WN) + u8 * 8;
 #pragma unroll
-        for (int q = 0; q < 4; q++)
-          if (n + q < p.N) row[n + q] = h[q];
+      for (int i = 0; i < TM; i++) {
+#pragma unroll
+        for (int j = 0; j < TN; j++) {
+          const f32x4_t c = acc[i][j];
+          *reinterpret_cast<u32x2_t *>(mine + r * (UNITS * 16) + (((j * 2 + (g >> 1)) ^ (r & (UNITS - 1))) * 16) + (g & 1) * 8) =
+              u32x2_t{pack2<F16>(c[0], c[1]), pack2<F16>(c[2], c[3])};
+        }
+#pragma unroll
+        for (int q = 0; q < 16 / ROWS; q++) {
+          const int rr = q * ROWS + row;
+          const u32x4_t o = *reinterpret_cast<const u32x4_t *>(mine + rr * (UNITS * 16) + ((u8 ^ (rr & (UNITS - 1))) * 16));
+          const int64_t m = t.m0 + wm * (BM / WM) + i * 16 + rr;
+          if (!row_is_stored<GROUPED>(p, t, m)) continue;
+          uint16_t *dst = static_cast<uint16_t *>(p.out) + m * p.ldo + n;
+          typedef u32x4_t U __attribute__((aligned(2)));
+          if (n + 8 <= p.N) {
+            __builtin_nontemporal_store(o, reinterpret_cast<U *>(dst));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+              if (n + e < p.N) dst[e] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+    if (!more) break;
+    t = next;
+    here = then;
+    at += stride;
+    v += nb;
+    gr = ng;
+    ch = nc;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // nothing may arrive in LDS that has another owner
+}
+
+// Rows of at most one block, and indexed rows that lie past 4 GB.
+//
+// A workgroup has TN tiles of 16 columns and up to TM tiles of 16 rows; its
+// W waves share the blocks of K among them (block b goes to wave b % W) and
+// load what they need from global memory straight into registers, U blocks at
+// a time, one such group ahead: 16 rows of 128 bytes are two loads of whole
+// 64-byte pieces. The sums of the waves meet in LDS, in the order of the waves.
+template <int TM, int TN, int W, int U, bool GROUPED, bool F16>
+__global__ __launch_bounds__(64 * W) void stream_kernel(GemmArgs p, uint32_t tiles_n) {
+  __shared__ float part[W][TM * TN][4][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int blocks = p.blocks;
+
+  Tile t;
+  const uint32_t tn = blockIdx.x % tiles_n, ty = blockIdx.x / tiles_n;
+  if constexpr (GROUPED) {
+    t.expert = ty;
+    int32_t lo, hi;
+    expert_rows(p, t.expert, &lo, &hi);
+    if (lo >= hi) return;
+    t.m0 = lo;
+    t.m1 = hi;
+  } else {
+    t.expert = 0;
+    t.m0 = (int64_t)ty * (16 * TM);
+    t.m1 = min(p.M, t.m0 + 16 * TM);
+  }
+  t.n0 = (int64_t)tn * (16 * TN);
+  const int64_t cb = (p.N + 127) / 128;
+  const uint8_t *w_at[TN];
+#pragma unroll
+  for (int j = 0; j < TN; j++) w_at[j] = p.w + ((int64_t)t.expert * p.N + min(t.n0 + j * 16 + r, p.N - 1)) * p.K;
+  const float *sw = p.w_scales + ((int64_t)t.expert * cb + t.n0 / 128) * blocks;     // 16 TN columns lie in one block
+
+  for (; t.m0 < t.m1; t.m0 += 16 * TM) {
+    const uint8_t *a_at[TM];
+    const float *sa[TM];
+#pragma unroll
+    for (int i = 0; i < TM; i++) {
+      const int64_t row = row_of_a<GROUPED>(p, t, t.m0 + i * 16 + r);
+      a_at[i] = p.a + row * p.K;
+      sa[i] = p.a_scales + row * blocks;
+    }
+    f32x4_t acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; i++)
+#pragma unroll
+      for (int j = 0; j < TN; j++) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+    struct Group {
+      u32x4_t w[U][TN][2], a[U][TM][2];
+      float s[U][TM];
+    };
+    // Blocks wave + W (first + u); past the end, or past the row's end, zeros.
+    auto fetch = [&](Group &q, int first) {
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const int b = wave + W * (first + u);
+        const bool in = b < blocks;
+        const int64_t k0 = (int64_t)(in ? b : 0) * 128;
+        const float c = sw[in ? b : 0];
+#pragma unroll
+        for (int i = 0; i < TM; i++) q.s[u][i] = in ? sa[i][in ? b : 0] * c : 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int64_t k = k0 + h * 64 + g * 16;
+          const bool has = in && k < p.K;
+          const int64_t at = has ? k : 0;
+#pragma unroll
+          for (int j = 0; j < TN; j++) q.w[u][j][h] = *reinterpret_cast<const u32x4_t *>(w_at[j] + at);
+#pragma unroll
+          for (int i = 0; i < TM; i++) {
+            const u32x4_t v = *reinterpret_cast<const u32x4_t *>(a_at[i] + at);
+            q.a[u][i][h] = has ? v : u32x4_t{0u, 0u, 0u, 0u};
+          }
+        }
+      }
+    };
+    auto meet = [&](const Group &q) {
+#pragma unroll
+      for (int u = 0; u < U; u++)
+#pragma unroll
+        for (int i = 0; i < TM; i++)
+#pragma unroll
+          for (int j = 0; j < TN; j++) {
+            const f32x4_t d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                join(q.w[u][j][0], q.w[u][j][1]), join(q.a[u][i][0], q.a[u][i][1]), f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(q.s[u][i], d[e], acc[i][j][e]);
+          }
+    };
+    const int mine = (blocks - wave + W - 1) / W;
+    Group q0, q1;
+    fetch(q0, 0);
+    for (int f = 0; f < mine; f += 2 * U) {
+      if (f + U < mine) fetch(q1, f + U);
+      meet(q0);
+      if (f + U < mine) {
+        if (f + 2 * U < mine) fetch(q0, f + 2 * U);
+        meet(q1);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TM; i++)
+#pragma unroll
+      for (int j = 0; j < TN; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) part[wave][i * TN + j][e][lane] = acc[i][j][e];
+    __syncthreads();
+    // Wave q sums tile q, q + W, ..: four columns of one row to a lane.
+    for (int q = wave; q < TM * TN; q += W) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        v[e] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; w++) v[e] += part[w][q][e][lane];
+      }
+      const int64_t m = t.m0 + q / TN * 16 + r, n = t.n0 + q % TN * 16 + g * 4;
+      if (row_is_stored<GROUPED>(p, t, m)) {
+        uint16_t *row = static_cast<uint16_t *>(p.out) + m * p.ldo;
+        typedef u32x2_t U2 __attribute__((aligned(2)));
+        const u32x2_t o = {pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3])};
+        if (n + 4 <= p.N) {
+          *reinterpret_cast<U2 *>(row + n) = o;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            if (n + e < p.N) row[n + e] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
+        }
+      }
+    }
+    __syncthreads();
   }
 }
 
-template <int BM, int BN, int WM, int WN, bool GROUPED>
-static nvfp4_status launch_tiles(GemmArgs a, int dtype, hipStream_t s) {
-  a.tiles_n = (int32_t)((a.N + BN - 1) / BN);
-  int64_t tm;
-  if (GROUPED) {
-    tm = a.M / BM + a.experts;            // every expert may end in a partial tile
-    if (tm > a.M) tm = a.M;
-  } else {
-    tm = (a.M + BM - 1) / BM;
+// The parts of K, added in their order: four columns to a thread.
+template <bool F16>
+__global__ __launch_bounds__(256) void add_parts_kernel(GemmArgs p) {
+  const int64_t quads = (p.N + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= p.M * quads) return;
+  const int64_t m = i / quads, n = (i - m * quads) * 4;
+  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int q = 0; q < p.parts; q++) {
+    const f32x4_t u = *reinterpret_cast<const f32x4_t *>(p.partial + ((int64_t)q * p.M + m) * quads * 4 + n);
+#pragma unroll
+    for (int e = 0; e < 4; e++) v[e] += u[e];
   }
+  const uint32_t lo = pack2<F16>(v[0], v[1]), hi = pack2<F16>(v[2], v[3]);
+  uint16_t *dst = static_cast<uint16_t *>(p.out) + m * p.ldo + n;
+  typedef u32x2_t U __attribute__((aligned(2)));
+  if (n + 4 <= p.N) {
+    *reinterpret_cast<U *>(dst) = u32x2_t{lo, hi};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (n + e < p.N) dst[e] = (uint16_t)((e < 2 ? lo : hi) >> (16 * (e & 1)));
+  }
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, bool SPLIT = false>
+static nvfp4_status launch_tiles(GemmArgs a, int dtype, int per_cu, hipStream_t s) {
+  a.tiles_n = (int32_t)((a.N + BN - 1) / BN);
+  // grouped: at most, every expert ending in a partial tile
+  const int64_t tm = GROUPED ? std::min(a.M, a.M / BM + a.experts) : (a.M + BM - 1) / BM;
   a.tiles_m = (int32_t)tm;
-  const int64_t tiles = tm * a.tiles_n;
+  const int64_t tiles = tm * a.tiles_n * (SPLIT ? a.parts : 1);
   if (tiles > 0x7FFFFF00) return NVFP4_ERR_SHAPE;
-  const unsigned grid = (unsigned)((tiles + 7) / 8 * 8);
+  const int64_t room = std::max(8, device_cus_or_default() / 8 * 8) * (int64_t)per_cu;
+  const unsigned grid = (unsigned)std::min(room, (tiles + 7) / 8 * 8);
   if (dtype == NVFP4_F16)
-    hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, 2, GROUPED, true>), dim3(grid), dim3(64 * WM * WN), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, STAGES, GROUPED, SPLIT, true>), dim3(grid), dim3(64 * WM * WN), 0, s, a);
   else
-    hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, 2, GROUPED, false>), dim3(grid), dim3(64 * WM * WN), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, STAGES, GROUPED, SPLIT, false>), dim3(grid), dim3(64 * WM * WN), 0, s, a);
+  NVFP4_LAUNCH_CHECK();
+  if constexpr (SPLIT) {
+    const unsigned adds = (unsigned)((a.M * ((a.N + 3) / 4) + 255) / 256);
+    if (dtype == NVFP4_F16)
+      hipLaunchKernelGGL((add_parts_kernel<true>), dim3(adds), dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((add_parts_kernel<false>), dim3(adds), dim3(256), 0, s, a);
+    NVFP4_LAUNCH_CHECK();
+  }
+  return NVFP4_OK;
+}
+
+template <int TM, int TN, int W, int U, bool GROUPED>
+static nvfp4_status launch_stream(const GemmArgs &a, int dtype, hipStream_t s) {
+  const int64_t tn = (a.N + 16 * TN - 1) / (16 * TN), ty = GROUPED ? a.experts : (a.M + 16 * TM - 1) / (16 * TM);
+  if (tn * ty > 0x7FFFFF00) return NVFP4_ERR_SHAPE;
+  const dim3 grid((unsigned)(tn * ty));
+  if (dtype == NVFP4_F16)
+    hipLaunchKernelGGL((stream_kernel<TM, TN, W, U, GROUPED, true>), grid, dim3(64 * W), 0, s, a, (uint32_t)tn);
+  else
+    hipLaunchKernelGGL((stream_kernel<TM, TN, W, U, GROUPED, false>), grid, dim3(64 * W), 0, s, a, (uint32_t)tn);
   NVFP4_LAUNCH_CHECK();
   return NVFP4_OK;
 }
 
+// The tile shapes, and what one block of K costs a workgroup of each (us, on 256
+// CUs; with few workgroups on the device, and with every place taken), measured
+// over products of 1 .. 8192 rows. Small tiles fill the device and hide memory's
+// latency behind four blocks in flight; large ones read less: a 64 x 64 tile
+// brings 16 KB for 64 products of its block, a 256 x 256 tile 64 KB for 1024.
+struct Shape {
+  int bm, bn, per_cu, stages;
+  float few, full;
+};
+constexpr Shape kShapes[] = {{32, 128, 1, 4, 0.50f, 0.66f},
+                             {64, 64, 2, 4, 0.38f, 0.52f},
+                             {64, 128, 2, 2, 0.70f, 0.95f},
+                             {128, 128, 2, 2, 0.78f, 1.25f},
+                             {256, 256, 1, 2, 1.60f, 1.75f}};
+constexpr int kWide = 4;                  // the last is never split
+constexpr int kMaxParts = 16;
+constexpr float kReadRate = 5.2e6f;       // bytes a us that weights stream at
+constexpr float kPartsRate = 5.0e6f;      // and FP32 parts, written and read
+
+struct Plan {
+  int shape = -1;     // -1: stream_kernel
+  int parts = 1;
+};
+
+// The shape, and the parts of K, of the least estimated time: whole rounds of
+// the device at the full cost, the last one at that of its filling, but no less
+// than the operands take to arrive. Splitting costs a second launch and FP32
+// sums through memory, and pays where the tiles alone leave CUs idle: one row
+// on 17408 x 5120 weights takes 21.5 us in four parts, 32 in two. Grouped:
+// rows is what an expert has on average.
+static Plan choose(int64_t M, int64_t N, int64_t K, int64_t experts, int cus) {
+  const int64_t blocks = (K + 127) / 128;
+  const float rows = (float)M / (float)std::max<int64_t>(1, experts);
+  Plan best;
+  float least = 0.0f;
+  for (int i = 0; i <= kWide; i++) {
+    const Shape &h = kShapes[i];
+    if (blocks < h.stages) continue;
+    const float tn = (float)((N + h.bn - 1) / h.bn);
+    const float tm = experts > 0 ? (float)experts * std::max(1.0f - expf(-rows), rows / h.bm + 0.5f * std::min(1.0f, rows / h.bm))
+                                 : (float)((M + h.bm - 1) / h.bm);
+    const float places = (float)(std::max(8, cus / 8 * 8) * h.per_cu);
+    const float met = experts > 0 ? (float)experts * (1.0f - expf(-rows)) : 1.0f;
+    const float arrive = ((float)M * K + met * N * K) / (kReadRate * cus / 256);
+    for (int parts = 1; parts <= (experts > 0 || i == kWide ? 1 : kMaxParts); parts++) {
+      if (parts > 1 && blocks / parts < 4) break;
+      const float rounds = tm * tn * parts / places, whole = floorf(rounds), rest = rounds - whole;
+      const float steps = (float)((blocks + parts - 1) / parts);
+      float t = steps * (whole * h.full + (rest > 0.0f ? h.few + (h.full - h.few) * rest : 0.0f));
+      t = std::max(t, arrive);
+      if (parts > 1) t += 2.5f + 8.0f * parts * M * N / kPartsRate;
+      if (best.shape < 0 || t < least) {
+        best.shape = i;
+        best.parts = parts;
+        least = t;
+      }
+    }
+  }
+  return best;
+}
+
+// Its loads' offsets are 32-bit, and it reads the last 128 bytes of a row as a whole.
+static bool tiles_fit(int64_t K, bool indexed, int64_t a_rows) {
+  return K >= 129 && K <= (1 << 23) && (!indexed || a_rows <= 0xFFFFFFE0ll / K);
+}
+
+static size_t parts_bytes(int64_t M, int64_t N, int parts) {
+  return parts > 1 ? (size_t)parts * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4 : 0;
+}
+
 template <bool GROUPED>
-static nvfp4_status launch(const GemmArgs &a, int dtype, hipStream_t s) {
-  return launch_tiles<128, 128, 2, 2, GROUPED>(a, dtype, s);
+static nvfp4_status launch(GemmArgs a, int dtype, Plan plan, hipStream_t s) {
+  a.parts = plan.parts;
+  if constexpr (!GROUPED) {
+    if (plan.parts > 1) {
+      switch (plan.shape) {
+        case 0: return launch_tiles<32, 128, 1, 4, 4, false, true>(a, dtype, kShapes[0].per_cu, s);
+        case 1: return launch_tiles<64, 64, 2, 2, 4, false, true>(a, dtype, kShapes[1].per_cu, s);
+        case 2: return launch_tiles<64, 128, 2, 2, 2, false, true>(a, dtype, kShapes[2].per_cu, s);
+        default: return launch_tiles<128, 128, 2, 2, 2, false, true>(a, dtype, kShapes[3].per_cu, s);
+      }
+    }
+  }
+  switch (plan.shape) {
+    case 0: return launch_tiles<32, 128, 1, 4, 4, GROUPED>(a, dtype, kShapes[0].per_cu, s);
+    case 1: return launch_tiles<64, 64, 2, 2, 4, GROUPED>(a, dtype, kShapes[1].per_cu, s);
+    case 2: return launch_tiles<64, 128, 2, 2, 2, GROUPED>(a, dtype, kShapes[2].per_cu, s);
+    case 3: return launch_tiles<128, 128, 2, 2, 2, GROUPED>(a, dtype, kShapes[3].per_cu, s);
+    case 4: return launch_tiles<256, 256, 2, 4, 2, GROUPED>(a, dtype, kShapes[4].per_cu, s);
+    default: return launch_stream<4, 2, 1, 1, GROUPED>(a, dtype, s);
+  }
 }
 
 static bool gemm_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t ldo) {
@@ -326,7 +781,14 @@ static bool gemm_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t ldo) {
 using namespace nvfp4;
 using namespace nvfp4::fp8;
 
-extern "C" size_t nvfp4_fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) { return 0; }
+static Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  return tiles_fit(K, false, 0) ? choose(M, N, K, 0, device_cus_or_default()) : Plan();
+}
+
+extern "C" size_t nvfp4_fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M < 1 || !gemm_sizes_ok(M, N, K, N)) return 0;
+  return parts_bytes(M, N, plan_of(M, N, K).parts);
+}
 
 extern "C" nvfp4_status nvfp4_fp8_gemm(const uint8_t *a, const float *a_scales, const uint8_t *w, const float *w_scales,
                                        int64_t M, int64_t N, int64_t K, void *out, int dtype, int64_t ldo, void *ws,
@@ -337,7 +799,8 @@ extern "C" nvfp4_status nvfp4_fp8_gemm(const uint8_t *a, const float *a_scales, 
   if (!a || !a_scales || !w || !w_scales || !out) return NVFP4_ERR_NULL;
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scales, 4) || !aligned(w_scales, 4) || !aligned(out, 2))
     return NVFP4_ERR_ALIGN;
-  const size_t need = nvfp4_fp8_gemm_workspace_bytes(M, N, K);
+  const Plan plan = plan_of(M, N, K);
+  const size_t need = parts_bytes(M, N, plan.parts);
   if (need > 0) {
     if (!ws || ws_bytes < need) return NVFP4_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return NVFP4_ERR_ALIGN;
@@ -356,7 +819,8 @@ extern "C" nvfp4_status nvfp4_fp8_gemm(const uint8_t *a, const float *a_scales, 
   p.ldo = ldo;
   p.blocks = (int32_t)((K + 127) / 128);
   p.a_rows = M;
-  return launch<false>(p, dtype, (hipStream_t)stream);
+  p.partial = static_cast<float *>(ws);
+  return launch<false>(p, dtype, plan, (hipStream_t)stream);
 }
 
 extern "C" nvfp4_status nvfp4_fp8_gemm_grouped(const uint8_t *a, const float *a_scales, int64_t a_rows,
@@ -389,5 +853,6 @@ extern "C" nvfp4_status nvfp4_fp8_gemm_grouped(const uint8_t *a, const float *a_
   p.rows = rows;
   p.a_rows = a_rows;
   p.experts = experts;
-  return launch<true>(p, dtype, (hipStream_t)stream);
+  const Plan plan = tiles_fit(K, rows != nullptr, a_rows) ? choose(M, N, K, experts, device_cus_or_default()) : Plan();
+  return launch<true>(p, dtype, plan, (hipStream_t)stream);
 }
