@@ -475,19 +475,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(GemmArgs p) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // nothing may arrive in LDS that has another owner
 }
 
-// Rows of at most one block, and indexed rows that lie past 4 GB.
-//
-// A workgroup has TN tiles of 16 columns and up to TM tiles of 16 rows; its
-// W waves share the blocks of K among them (block b goes to wave b % W) and
-// load what they need from global memory straight into registers, U blocks at
-// a time, one such group ahead: 16 rows of 128 bytes are two loads of whole
-// 64-byte pieces. The sums of the waves meet in LDS, in the order of the waves.
-template <int TM, int TN, int W, int U, bool GROUPED, bool F16>
-__global__ __launch_bounds__(64 * W) void stream_kernel(GemmArgs p, uint32_t tiles_n) {
-  __shared__ float part[W][TM * TN][4][64];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, g = lane >> 4;
+// What tile_kernel does not take: rows of one block, rows longer than its
+// offsets reach (K over 2^23), indexed rows past 4 GB. One wave has 64 rows and
+// 32 columns (grouped: the rows of an expert, 64 at a time) and loads what it
+// needs straight into registers, through 64-bit addresses, one block ahead; 16
+// rows of 128 bytes are two loads of whole 64-byte pieces. Nothing is shared, so
+// what bounds it is memory's latency.
+template <bool GROUPED, bool F16>
+__global__ __launch_bounds__(64) void stream_kernel(GemmArgs p, uint32_t tiles_n) {
+  constexpr int TM = 4, TN = 2;
+  const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
   const int blocks = p.blocks;
 
   Tile t;
@@ -496,7 +493,6 @@ __global__ __launch_bounds__(64 * W) void stream_kernel(GemmArgs p, uint32_t til
     t.expert = ty;
     int32_t lo, hi;
     expert_rows(p, t.expert, &lo, &hi);
-    if (lo >= hi) return;
     t.m0 = lo;
     t.m1 = hi;
   } else {
@@ -509,7 +505,7 @@ __global__ __launch_bounds__(64 * W) void stream_kernel(GemmArgs p, uint32_t til
   const uint8_t *w_at[TN];
 #pragma unroll
   for (int j = 0; j < TN; j++) w_at[j] = p.w + ((int64_t)t.expert * p.N + min(t.n0 + j * 16 + r, p.N - 1)) * p.K;
-  const float *sw = p.w_scales + ((int64_t)t.expert * cb + t.n0 / 128) * blocks;     // 16 TN columns lie in one block
+  const float *sw = p.w_scales + ((int64_t)t.expert * cb + t.n0 / 128) * blocks;     // the columns lie in one block
 
   for (; t.m0 < t.m1; t.m0 += 16 * TM) {
     const uint8_t *a_at[TM];
@@ -526,90 +522,70 @@ __global__ __launch_bounds__(64 * W) void stream_kernel(GemmArgs p, uint32_t til
 #pragma unroll
       for (int j = 0; j < TN; j++) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-    struct Group {
-      u32x4_t w[U][TN][2], a[U][TM][2];
-      float s[U][TM];
+    struct Block {
+      u32x4_t w[TN][2], a[TM][2];
+      float s[TM];
     };
-    // Blocks wave + W (first + u); past the end, or past the row's end, zeros.
-    auto fetch = [&](Group &q, int first) {
+    auto fetch = [&](Block &q, int b) {      // zeros of A behind the row's end
+      const float c = sw[b];
 #pragma unroll
-      for (int u = 0; u < U; u++) {
-        const int b = wave + W * (first + u);
-        const bool in = b < blocks;
-        const int64_t k0 = (int64_t)(in ? b : 0) * 128;
-        const float c = sw[in ? b : 0];
+      for (int i = 0; i < TM; i++) q.s[i] = sa[i][b] * c;
 #pragma unroll
-        for (int i = 0; i < TM; i++) q.s[u][i] = in ? sa[i][in ? b : 0] * c : 0.0f;
+      for (int h = 0; h < 2; h++) {
+        const int64_t k = (int64_t)b * 128 + h * 64 + g * 16;
+        const bool has = k < p.K;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const int64_t k = k0 + h * 64 + g * 16;
-          const bool has = in && k < p.K;
-          const int64_t at = has ? k : 0;
+        for (int j = 0; j < TN; j++) {
+          const u32x4_t v = *reinterpret_cast<const u32x4_t *>(w_at[j] + (has ? k : 0));
+          q.w[j][h] = has ? v : u32x4_t{0u, 0u, 0u, 0u};
+        }
 #pragma unroll
-          for (int j = 0; j < TN; j++) q.w[u][j][h] = *reinterpret_cast<const u32x4_t *>(w_at[j] + at);
-#pragma unroll
-          for (int i = 0; i < TM; i++) {
-            const u32x4_t v = *reinterpret_cast<const u32x4_t *>(a_at[i] + at);
-            q.a[u][i][h] = has ? v : u32x4_t{0u, 0u, 0u, 0u};
-          }
+        for (int i = 0; i < TM; i++) {
+          const u32x4_t v = *reinterpret_cast<const u32x4_t *>(a_at[i] + (has ? k : 0));
+          q.a[i][h] = has ? v : u32x4_t{0u, 0u, 0u, 0u};
         }
       }
     };
-    auto meet = [&](const Group &q) {
+    auto meet = [&](const Block &q) {
 #pragma unroll
-      for (int u = 0; u < U; u++)
+      for (int i = 0; i < TM; i++)
 #pragma unroll
-        for (int i = 0; i < TM; i++)
+        for (int j = 0; j < TN; j++) {
+          const f32x4_t d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(q.w[j][0], q.w[j][1]), join(q.a[i][0], q.a[i][1]),
+                                                                             f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
 #pragma unroll
-          for (int j = 0; j < TN; j++) {
-            const f32x4_t d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                join(q.w[u][j][0], q.w[u][j][1]), join(q.a[u][i][0], q.a[u][i][1]), f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(q.s[u][i], d[e], acc[i][j][e]);
-          }
+          for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(q.s[i], d[e], acc[i][j][e]);
+        }
     };
-    const int mine = (blocks - wave + W - 1) / W;
-    Group q0, q1;
+    Block q0, q1;
     fetch(q0, 0);
-    for (int f = 0; f < mine; f += 2 * U) {
-      if (f + U < mine) fetch(q1, f + U);
+    for (int b = 0; b < blocks; b += 2) {
+      if (b + 1 < blocks) fetch(q1, b + 1);
       meet(q0);
-      if (f + U < mine) {
-        if (f + 2 * U < mine) fetch(q0, f + 2 * U);
+      if (b + 1 < blocks) {
+        if (b + 2 < blocks) fetch(q0, b + 2);
         meet(q1);
       }
     }
 #pragma unroll
-    for (int i = 0; i < TM; i++)
+    for (int i = 0; i < TM; i++) {
+      const int64_t m = t.m0 + i * 16 + r;
+      if (!row_is_stored<GROUPED>(p, t, m)) continue;
 #pragma unroll
-      for (int j = 0; j < TN; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) part[wave][i * TN + j][e][lane] = acc[i][j][e];
-    __syncthreads();
-    // Wave q sums tile q, q + W, ..: four columns of one row to a lane.
-    for (int q = wave; q < TM * TN; q += W) {
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; e++) {
-        v[e] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; w++) v[e] += part[w][q][e][lane];
-      }
-      const int64_t m = t.m0 + q / TN * 16 + r, n = t.n0 + q % TN * 16 + g * 4;
-      if (row_is_stored<GROUPED>(p, t, m)) {
-        uint16_t *row = static_cast<uint16_t *>(p.out) + m * p.ldo;
+      for (int j = 0; j < TN; j++) {
+        const int64_t n = t.n0 + j * 16 + g * 4;
+        uint16_t *dst = static_cast<uint16_t *>(p.out) + m * p.ldo + n;
         typedef u32x2_t U2 __attribute__((aligned(2)));
-        const u32x2_t o = {pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3])};
+        const u32x2_t o = {pack2<F16>(acc[i][j][0], acc[i][j][1]), pack2<F16>(acc[i][j][2], acc[i][j][3])};
         if (n + 4 <= p.N) {
-          *reinterpret_cast<U2 *>(row + n) = o;
+          *reinterpret_cast<U2 *>(dst) = o;
         } else {
 #pragma unroll
           for (int e = 0; e < 4; e++)
-            if (n + e < p.N) row[n + e] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
+            if (n + e < p.N) dst[e] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
         }
       }
     }
-    __syncthreads();
   }
 }
 
@@ -664,37 +640,39 @@ static nvfp4_status launch_tiles(GemmArgs a, int dtype, int per_cu, hipStream_t 
   return NVFP4_OK;
 }
 
-template <int TM, int TN, int W, int U, bool GROUPED>
+template <bool GROUPED>
 static nvfp4_status launch_stream(const GemmArgs &a, int dtype, hipStream_t s) {
-  const int64_t tn = (a.N + 16 * TN - 1) / (16 * TN), ty = GROUPED ? a.experts : (a.M + 16 * TM - 1) / (16 * TM);
+  const int64_t tn = (a.N + 31) / 32, ty = GROUPED ? a.experts : (a.M + 63) / 64;
   if (tn * ty > 0x7FFFFF00) return NVFP4_ERR_SHAPE;
   const dim3 grid((unsigned)(tn * ty));
   if (dtype == NVFP4_F16)
-    hipLaunchKernelGGL((stream_kernel<TM, TN, W, U, GROUPED, true>), grid, dim3(64 * W), 0, s, a, (uint32_t)tn);
+    hipLaunchKernelGGL((stream_kernel<GROUPED, true>), grid, dim3(64), 0, s, a, (uint32_t)tn);
   else
-    hipLaunchKernelGGL((stream_kernel<TM, TN, W, U, GROUPED, false>), grid, dim3(64 * W), 0, s, a, (uint32_t)tn);
+    hipLaunchKernelGGL((stream_kernel<GROUPED, false>), grid, dim3(64), 0, s, a, (uint32_t)tn);
   NVFP4_LAUNCH_CHECK();
   return NVFP4_OK;
 }
 
 // The tile shapes, and what one block of K costs a workgroup of each (us, on 256
-// CUs; with few workgroups on the device, and with every place taken), measured
-// over products of 1 .. 8192 rows. Small tiles fill the device and hide memory's
-// latency behind four blocks in flight; large ones read less: a 64 x 64 tile
-// brings 16 KB for 64 products of its block, a 256 x 256 tile 64 KB for 1024.
+// CUs; with few workgroups on the device, and with every place taken). Small
+// tiles fill the device and hide memory's latency behind four blocks in flight;
+// large ones read less: a 64 x 64 tile brings 16 KB for 64 products of its
+// block, a 256 x 256 tile 64 KB for 1024. Rows of the few that an expert often
+// has waste least of 32 x 128; dense, it was within 6 % of the others at best.
 struct Shape {
   int bm, bn, per_cu, stages;
   float few, full;
+  bool dense, grouped, split;
 };
-constexpr Shape kShapes[] = {{32, 128, 1, 4, 0.50f, 0.66f},
-                             {64, 64, 2, 4, 0.38f, 0.52f},
-                             {64, 128, 2, 2, 0.70f, 0.95f},
-                             {128, 128, 2, 2, 0.78f, 1.25f},
-                             {256, 256, 1, 2, 1.60f, 1.75f}};
-constexpr int kWide = 4;                  // the last is never split
+constexpr Shape kShapes[] = {{32, 128, 1, 4, 0.52f, 0.52f, false, true, false},
+                             {64, 64, 2, 4, 0.28f, 0.70f, true, true, true},
+                             {64, 128, 2, 2, 0.85f, 0.85f, true, true, false},
+                             {128, 128, 2, 2, 0.90f, 1.20f, true, false, true},
+                             {256, 256, 1, 2, 2.00f, 1.90f, true, true, false}};
 constexpr int kMaxParts = 16;
-constexpr float kReadRate = 5.2e6f;       // bytes a us that weights stream at
-constexpr float kPartsRate = 5.0e6f;      // and FP32 parts, written and read
+constexpr float kReadRate = 3.8e6f;       // bytes a us that operands stream at
+constexpr float kPartsTime = 4.0f;        // us of the second launch
+constexpr float kPartsRate = 3.5e6f;      // and bytes a us of the FP32 parts, written and read
 
 struct Plan {
   int shape = -1;     // -1: stream_kernel
@@ -704,30 +682,33 @@ struct Plan {
 // The shape, and the parts of K, of the least estimated time: whole rounds of
 // the device at the full cost, the last one at that of its filling, but no less
 // than the operands take to arrive. Splitting costs a second launch and FP32
-// sums through memory, and pays where the tiles alone leave CUs idle: one row
-// on 17408 x 5120 weights takes 21.5 us in four parts, 32 in two. Grouped:
-// rows is what an expert has on average.
+// sums through memory, and pays where the tiles alone leave CUs idle: 61 rows on
+// 5120 x 17408 weights take 27 us in three parts of K, 63 in one. The figures
+// above are fitted to 107 products (1 .. 24576 rows, 1 .. 128 experts, K 272 ..
+// 17408) in every shape and up to 16 parts: what this picks is 2 % over the best
+// of them in the mean, 24 % at most. Grouped: rows is what an expert has on
+// average.
 static Plan choose(int64_t M, int64_t N, int64_t K, int64_t experts, int cus) {
   const int64_t blocks = (K + 127) / 128;
   const float rows = (float)M / (float)std::max<int64_t>(1, experts);
+  const float met = experts > 0 ? (float)experts * (1.0f - expf(-rows)) : 1.0f;      // experts with rows
+  const float arrive = ((float)M * K + met * N * K) / (kReadRate * cus / 256);
   Plan best;
   float least = 0.0f;
-  for (int i = 0; i <= kWide; i++) {
+  for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); i++) {
     const Shape &h = kShapes[i];
-    if (blocks < h.stages) continue;
+    if (blocks < h.stages || !(experts > 0 ? h.grouped : h.dense)) continue;
     const float tn = (float)((N + h.bn - 1) / h.bn);
-    const float tm = experts > 0 ? (float)experts * std::max(1.0f - expf(-rows), rows / h.bm + 0.5f * std::min(1.0f, rows / h.bm))
+    const float tm = experts > 0 ? std::max(met, (float)experts * (rows / h.bm + 0.5f * std::min(1.0f, rows / h.bm)))
                                  : (float)((M + h.bm - 1) / h.bm);
     const float places = (float)(std::max(8, cus / 8 * 8) * h.per_cu);
-    const float met = experts > 0 ? (float)experts * (1.0f - expf(-rows)) : 1.0f;
-    const float arrive = ((float)M * K + met * N * K) / (kReadRate * cus / 256);
-    for (int parts = 1; parts <= (experts > 0 || i == kWide ? 1 : kMaxParts); parts++) {
+    for (int parts = 1; parts <= (experts == 0 && h.split ? kMaxParts : 1); parts++) {
       if (parts > 1 && blocks / parts < 4) break;
       const float rounds = tm * tn * parts / places, whole = floorf(rounds), rest = rounds - whole;
       const float steps = (float)((blocks + parts - 1) / parts);
       float t = steps * (whole * h.full + (rest > 0.0f ? h.few + (h.full - h.few) * rest : 0.0f));
       t = std::max(t, arrive);
-      if (parts > 1) t += 2.5f + 8.0f * parts * M * N / kPartsRate;
+      if (parts > 1) t += kPartsTime + 8.0f * parts * M * N / kPartsRate;
       if (best.shape < 0 || t < least) {
         best.shape = i;
         best.parts = parts;
@@ -747,27 +728,26 @@ static size_t parts_bytes(int64_t M, int64_t N, int parts) {
   return parts > 1 ? (size_t)parts * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4 : 0;
 }
 
-template <bool GROUPED>
-static nvfp4_status launch(GemmArgs a, int dtype, Plan plan, hipStream_t s) {
+static nvfp4_status launch_dense(GemmArgs a, int dtype, Plan plan, hipStream_t s) {
   a.parts = plan.parts;
-  if constexpr (!GROUPED) {
-    if (plan.parts > 1) {
-      switch (plan.shape) {
-        case 0: return launch_tiles<32, 128, 1, 4, 4, false, true>(a, dtype, kShapes[0].per_cu, s);
-        case 1: return launch_tiles<64, 64, 2, 2, 4, false, true>(a, dtype, kShapes[1].per_cu, s);
-        case 2: return launch_tiles<64, 128, 2, 2, 2, false, true>(a, dtype, kShapes[2].per_cu, s);
-        default: return launch_tiles<128, 128, 2, 2, 2, false, true>(a, dtype, kShapes[3].per_cu, s);
-      }
-    }
-  }
-  switch (plan.shape) {
-    case 0: return launch_tiles<32, 128, 1, 4, 4, GROUPED>(a, dtype, kShapes[0].per_cu, s);
-    case 1: return launch_tiles<64, 64, 2, 2, 4, GROUPED>(a, dtype, kShapes[1].per_cu, s);
-    case 2: return launch_tiles<64, 128, 2, 2, 2, GROUPED>(a, dtype, kShapes[2].per_cu, s);
-    case 3: return launch_tiles<128, 128, 2, 2, 2, GROUPED>(a, dtype, kShapes[3].per_cu, s);
-    case 4: return launch_tiles<256, 256, 2, 4, 2, GROUPED>(a, dtype, kShapes[4].per_cu, s);
-    default: return launch_stream<4, 2, 1, 1, GROUPED>(a, dtype, s);
-  }
+  if (plan.shape == 1)
+    return plan.parts > 1 ? launch_tiles<64, 64, 2, 2, 4, false, true>(a, dtype, kShapes[1].per_cu, s)
+                          : launch_tiles<64, 64, 2, 2, 4, false>(a, dtype, kShapes[1].per_cu, s);
+  if (plan.shape == 2) return launch_tiles<64, 128, 2, 2, 2, false>(a, dtype, kShapes[2].per_cu, s);
+  if (plan.shape == 3)
+    return plan.parts > 1 ? launch_tiles<128, 128, 2, 2, 2, false, true>(a, dtype, kShapes[3].per_cu, s)
+                          : launch_tiles<128, 128, 2, 2, 2, false>(a, dtype, kShapes[3].per_cu, s);
+  if (plan.shape == 4) return launch_tiles<256, 256, 2, 4, 2, false>(a, dtype, kShapes[4].per_cu, s);
+  return launch_stream<false>(a, dtype, s);
+}
+
+static nvfp4_status launch_grouped(GemmArgs a, int dtype, Plan plan, hipStream_t s) {
+  a.parts = 1;
+  if (plan.shape == 0) return launch_tiles<32, 128, 1, 4, 4, true>(a, dtype, kShapes[0].per_cu, s);
+  if (plan.shape == 1) return launch_tiles<64, 64, 2, 2, 4, true>(a, dtype, kShapes[1].per_cu, s);
+  if (plan.shape == 2) return launch_tiles<64, 128, 2, 2, 2, true>(a, dtype, kShapes[2].per_cu, s);
+  if (plan.shape == 4) return launch_tiles<256, 256, 2, 4, 2, true>(a, dtype, kShapes[4].per_cu, s);
+  return launch_stream<true>(a, dtype, s);
 }
 
 static bool gemm_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t ldo) {
@@ -820,7 +800,7 @@ extern "C" nvfp4_status nvfp4_fp8_gemm(const uint8_t *a, const float *a_scales, 
   p.blocks = (int32_t)((K + 127) / 128);
   p.a_rows = M;
   p.partial = static_cast<float *>(ws);
-  return launch<false>(p, dtype, plan, (hipStream_t)stream);
+  return launch_dense(p, dtype, plan, (hipStream_t)stream);
 }
 
 extern "C" nvfp4_status nvfp4_fp8_gemm_grouped(const uint8_t *a, const float *a_scales, int64_t a_rows,
@@ -854,5 +834,5 @@ extern "C" nvfp4_status nvfp4_fp8_gemm_grouped(const uint8_t *a, const float *a_
   p.a_rows = a_rows;
   p.experts = experts;
   const Plan plan = tiles_fit(K, rows != nullptr, a_rows) ? choose(M, N, K, experts, device_cus_or_default()) : Plan();
-  return launch<true>(p, dtype, plan, (hipStream_t)stream);
+  return launch_grouped(p, dtype, plan, (hipStream_t)stream);
 }
