@@ -83,14 +83,21 @@ __device__ __forceinline__ u32x2_t codes8(const float (&x)[8], Scale k) {
   return c;
 }
 
-// silu(g) u = g / (1 + e^-g) u. e^-g is bounded by 2^126 so that the quotient's
-// remainder stays finite (below g = -87 the result is under 2^-119 either way,
-// less than the smallest scale). The quotient by the same two steps, after one
-// that makes the reciprocal exact to half an ulp.
+// silu(g) u = g / (1 + e^-g) u. With t = RN(-g log2 e) and what that rounding
+// lost, l (exact but for 2^-48 of t), e^-g = 2^t (1 + l ln 2). g is taken within
+// -87 .. 104 there: above, 1 + e^-g is 1; below, the result is under 2^-119
+// either way, less than the smallest scale. The reciprocal is good to an ulp and
+// the quotient, after one step with its remainder, to hardly more than half of
+// one. The arithmetic counts here: with the library's expf and a division by a
+// corrected reciprocal, 2048 rows of 2 x 17408 BF16 columns took 47.6 us, now 41.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  const float d = 1.0f + fminf(expf(-g), 0x1p126f);
-  float r = __builtin_amdgcn_rcpf(d);
-  r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  const float c = __builtin_amdgcn_fmed3f(g, -87.0f, 104.0f);
+  const float t = c * -kLog2e;
+  const float l = __builtin_fmaf(c, -kLog2eRest, __builtin_fmaf(c, -kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  const float d = 1.0f + __builtin_fmaf(e, l * kLn2, e);
+  const float r = __builtin_amdgcn_rcpf(d);
   const float q = g * r;
   return __builtin_fmaf(__builtin_fmaf(-q, d, g), r, q) * u;
 }
@@ -106,8 +113,10 @@ struct RowsArgs {
 };
 
 // Sixteen lanes have a block of 128 columns, eight columns each; a thread has U
-// blocks, whose loads are all in flight before the first is used. K % 16 == 0:
-// a lane's eight columns are all there or none is.
+// blocks, whose loads are all in flight before the first is used (two: one, three
+// and four are 1 to 8 % slower). K % 16 == 0: a lane's eight columns are all
+// there or none is. Bound by HBM: 2048 rows of 34816 BF16 columns, 214 MB read
+// and written, take 40 us (5.3 TB/s); gated into 17408, 178 MB, 41 us (4.3).
 constexpr int kThreads = 256;
 
 template <int DT, bool GATED, int U>
@@ -162,7 +171,8 @@ struct WeightArgs {
 };
 
 // A workgroup has one block: 16 rows at a time, sixteen lanes to a row, the
-// whole block in registers between the maximum and the codes.
+// whole block in registers between the maximum and the codes. Bound by HBM:
+// 17408 x 5120 of BF16, 267 MB, take 55 us (4.8 TB/s).
 template <int DT>
 __global__ __launch_bounds__(kThreads) void weight_kernel(WeightArgs a) {
   constexpr int ES = DT == NVFP4_F32 ? 4 : 2;

@@ -85,9 +85,10 @@ def test_quantize_rows(rows, cols, pad, kind):
 @pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("rows,cols,pad", [(1, 16, 0), (2, 128, 0), (33, 1040, 8), (300, 272, 3)])
 def test_quantize_gated_rows(rows, cols, pad, kind):
-    """silu(g) u in FP32 is off by a few units of 2^-24: e^-g by one and a half, the sum, the reciprocal's two steps, the
-    quotient and the product by half each: under 2^-21 of the value. The scale then is off by that and its own half
-    step, and a code's value by half a step of E4M3 (2^-4 of the value, at least 2^-10 of a scale) and that."""
+    """silu(g) u in FP32 is off by a few units of 2^-24: e^-g by three (2^t by an ulp, its correction by half of one), the
+    sum by one, the corrected quotient by one and a little, the product by one: under 2^-21 of the value. The scale then is
+    off by that and its own half step, and a code's value by half a step of E4M3 (2^-4 of the value, at least 2^-10 of a
+    scale) and that."""
     r = rng(rows * cols)
     x = torch.from_numpy(np.concatenate([r.standard_normal((rows, cols)) * 4, r.standard_normal((rows, cols))], 1)).to(TYPES[kind])
     x[0, :4] = torch.tensor([-100.0, -88.0, 60.0, 0.0]).to(x.dtype)
