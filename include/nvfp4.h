@@ -552,7 +552,10 @@ nvfp4_status nvfp4_fp8_quantize_weight(const void *w, int dtype, int64_t experts
  *  M >= 0 (0 is a no-op), any N >= 1, K % 16 == 0.
  *  ws   nvfp4_fp8_gemm_workspace_bytes(M, N, K) bytes on the current device,
  *       16-byte aligned, not initialised; one per stream that runs
- *       concurrently. May be NULL when that is 0. */
+ *       concurrently. May be NULL when that is 0. Few rows on long ones are
+ *       summed in up to 16 parts of K (how many depends on the device's CUs),
+ *       which the workspace holds and which are added in their order: on one
+ *       kind of device a call gives the same bits every time. */
 size_t nvfp4_fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 nvfp4_status nvfp4_fp8_gemm(const uint8_t *a, const float *a_scales, const uint8_t *w, const float *w_scales, int64_t M,
                             int64_t N, int64_t K, void *out, int dtype, int64_t ldo, void *ws, size_t ws_bytes,

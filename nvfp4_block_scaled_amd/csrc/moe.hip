@@ -130,9 +130,7 @@ __global__ __launch_bounds__(THREADS) void place_kernel(SortArgs a) {
     scan(total, before);
   }
 
-  // One pass takes THREADS * kRounds pairs: each wave kRounds runs of 64. ONE: the pairs of all
-  // passes are counted before any is placed, so the ranks are found twice when there is more than one.
-  const uint32_t step = THREADS * kRounds;
+  // One pass takes THREADS * kRounds pairs: each wave kRounds runs of 64.
   int e[kRounds], rank[kRounds];
   auto pass = [&](uint32_t at) {
     for (int i = tid; i < WAVES * E; i += THREADS) lds[i] = 0;
@@ -184,31 +182,19 @@ __global__ __launch_bounds__(THREADS) void place_kernel(SortArgs a) {
     __syncthreads();
   };
 
-  if (ONE) {
+  if (ONE) {      // at most one pass
+    pass(0);
     int total[PER], none[PER];
 #pragma unroll
-    for (int q = 0; q < PER; q++) total[q] = none[q] = 0;
-    for (uint32_t at = 0;; at += step) {
-      pass(at);
-#pragma unroll
-      for (int q = 0; q < PER; q++) {
-        const int x = PER * tid + q;
-        for (int w = 0; w < WAVES; w++) total[q] += x < E ? lds[w * E + x] : 0;
-      }
-      if (at + step >= end || at + step < at) break;
-      __syncthreads();
+    for (int q = 0; q < PER; q++) {
+      const int x = PER * tid + q;
+      total[q] = none[q] = 0;
+      for (int w = 0; w < WAVES; w++) total[q] += x < E ? lds[w * E + x] : 0;
     }
     scan(total, none);
-    if (step >= end) {
-      place(0);
-    } else {
-      for (uint32_t at = 0; at < end; at += step) {
-        pass(at);
-        place(at);
-      }
-    }
+    place(0);
   } else {
-    for (uint32_t at = from; at < end; at += step) {
+    for (uint32_t at = from; at < end; at += THREADS * kRounds) {
       pass(at);
       place(at);
     }
@@ -453,10 +439,13 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a
 
 // ---------------------------------------------------------------- host side
 
-// How the pairs are cut: one workgroup of 1024 threads for up to kOnePairs (and
-// as many experts as its 16 histograms fit in 64 KB of LDS with), else chunks
-// of whole passes of 256 threads, at most kMaxChunks of them.
-constexpr int64_t kOnePairs = 8192, kOneExperts = 896;
+// How the pairs are cut: one workgroup of 1024 threads for what it places in one
+// pass (and as many experts as its 16 histograms fit in 64 KB of LDS with), else
+// chunks of whole passes of 256 threads, at most kMaxChunks of them. One
+// workgroup against two launches, 64 experts: 136 pairs 4.9 and 5.9 us, 4096
+// 6.9 and 7.3; with a second pass, 8192, 16.6 and 9.3. 262144 pairs take 31 us:
+// latency, of the counts' read and of four passes a chunk.
+constexpr int64_t kOnePairs = 1024 * kRounds, kOneExperts = 896;
 constexpr int kMaxChunks = 256;
 
 static bool one_workgroup(int64_t pairs, int64_t experts) { return pairs <= kOnePairs && experts <= kOneExperts; }

@@ -27,6 +27,10 @@ What is computed, with the passage each part follows:
   scales flip code signs, prepared size N*K/2 + N*K/16).
 * ``kv``       -- the key/value cache: page layout, append with rotary positions,
   attention in float64, page management.
+* ``fp8``      -- E4M3 matrices with block scales: both quantizers in binary32 as the
+  library defines them, products in float64, dense and by expert.
+* ``moe``      -- the sort of (token, choice) pairs by expert, rows to their places and
+  back, and the gradients, pair by pair in float64.
 
 Everything here is deliberately slow and plain: numpy, float64 or exact
 integers, no blocking or fusion beyond what the definitions state.

@@ -56,6 +56,14 @@ def test_rows_past_the_cache(T, top, width, dtype, pad):
     assert bool((room[used:] == 9.0).all()) and bool((room[:, width:] == 9.0).all())
 
 
+@pytest.mark.parametrize("T,top,experts", [(1023, 4, 64), (4096, 1, 896), (4096, 1, 897), (4097, 1, 64), (40000, 8, 100), (1, 5000, 3)])
+def test_sorts_around_the_passes(T, top, experts):
+    """What one workgroup places in a pass and a pair more; chunks of two passes; one token with many choices."""
+    ids = np.random.default_rng(T).integers(-1, experts + 1, (T, top)).astype(np.int32)
+    for got, want in zip(nv.nvfp4_moe_sort(torch.from_numpy(ids).cuda(), experts), moe.sort(ids, experts)):
+        np.testing.assert_array_equal(got.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("T,experts", [(40, 60), (5000, 300)])
 def test_two_dispatches_at_once(T, experts):
     g = torch.Generator("cuda").manual_seed(T)
