@@ -24,12 +24,24 @@ constexpr float kTop = 448.0f;
 constexpr uint32_t kLeastBits = 0x0D800000u;      // 2^-100
 constexpr uint32_t kInfBits = 0x7F800000u;
 
+// Inputs of over 64 MB (FAR) are read, and codes always written, past the caches
+// (nontemporal): a large input has mostly left them, and what it would push out
+// is worth more. Gated rows of 2 x 17408 BF16: 2048 38.9 -> 35.9 us, 8192 137 -> 130
+// (after a kernel that wrote them 248 -> 200); of inputs, 84 MB gain 8 % by it, 36
+// MB lose 3 to 7 %. Codes so written are read back by the next kernel as fast.
+constexpr int64_t kNear = int64_t(64) << 20;
+
+template <bool FAR, typename U>
+__device__ __forceinline__ U fetch(const U *p) {
+  return FAR ? __builtin_nontemporal_load(p) : *p;
+}
+
 // Eight consecutive elements of a row as FP32 values (exact); rows start at any element.
-template <int DT>
+template <int DT, bool FAR>
 __device__ __forceinline__ void load8(const void *p, float (&x)[8]) {
   if constexpr (DT == NVFP4_F32) {
     typedef f32x4_t U __attribute__((aligned(4)));
-    const f32x4_t a = static_cast<const U *>(p)[0], b = static_cast<const U *>(p)[1];
+    const f32x4_t a = fetch<FAR>(static_cast<const U *>(p)), b = fetch<FAR>(static_cast<const U *>(p) + 1);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       x[i] = a[i];
@@ -37,7 +49,7 @@ __device__ __forceinline__ void load8(const void *p, float (&x)[8]) {
     }
   } else {
     typedef u32x4_t U __attribute__((aligned(2)));
-    const u32x4_t w = *static_cast<const U *>(p);
+    const u32x4_t w = fetch<FAR>(static_cast<const U *>(p));
     unpack8<DT == NVFP4_F16>(w, x);
   }
 }
@@ -72,7 +84,7 @@ __device__ __forceinline__ float quotient(float x, Scale k) {
   return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q, k.s, x), k.r, q), x);
 }
 
-__device__ __forceinline__ u32x2_t codes8(const float (&x)[8], Scale k) {
+__device__ __forceinline__ void store8(uint8_t *to, const float (&x)[8], Scale k) {
   u32x2_t c;
 #pragma unroll
   for (int h = 0; h < 2; h++) {
@@ -80,7 +92,7 @@ __device__ __forceinline__ u32x2_t codes8(const float (&x)[8], Scale k) {
     w = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(x[4 * h + 2], k), quotient(x[4 * h + 3], k), w, true);
     c[h] = (uint32_t)w;
   }
-  return c;
+  __builtin_nontemporal_store(c, reinterpret_cast<u32x2_t *>(to));
 }
 
 // silu(g) u = g / (1 + e^-g) u. With t = RN(-g log2 e) and what that rounding
@@ -89,7 +101,7 @@ __device__ __forceinline__ u32x2_t codes8(const float (&x)[8], Scale k) {
 // either way, less than the smallest scale. The reciprocal is good to an ulp and
 // the quotient, after one step with its remainder, to hardly more than half of
 // one. The arithmetic counts here: with the library's expf and a division by a
-// corrected reciprocal, 2048 rows of 2 x 17408 BF16 columns took 47.6 us, now 41.
+// corrected reciprocal, 2048 rows of 2 x 17408 BF16 columns took 47.6 us, so 41.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
   const float c = __builtin_amdgcn_fmed3f(g, -87.0f, 104.0f);
@@ -116,12 +128,13 @@ struct RowsArgs {
 // blocks, whose loads are all in flight before the first is used (two: one, three
 // and four are 1 to 8 % slower). K % 16 == 0: a lane's eight columns are all
 // there or none is. Bound by HBM: 2048 rows of 34816 BF16 columns, 214 MB read
-// and written, take 40 us (5.3 TB/s); gated into 17408, 178 MB, 41 us (4.3).
-constexpr int kThreads = 256;
+// and written, take 39 us (5.5 TB/s); gated into 17408, 178 MB, 36 to 39 (4.6 and
+// more; the vector units are as busy then).
+constexpr int kThreads = 256, kRowBlocks = 2;
 
-template <int DT, bool GATED, int U>
+template <int DT, bool GATED, bool FAR>
 __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a) {
-  constexpr int ES = DT == NVFP4_F32 ? 4 : 2;
+  constexpr int ES = DT == NVFP4_F32 ? 4 : 2, U = kRowBlocks;
   const int l = threadIdx.x & 15;
   const int64_t first = (int64_t)blockIdx.x * (kThreads / 16 * U) + (threadIdx.x >> 4);
   float x[U][8], up[GATED ? U : 1][8];
@@ -141,8 +154,8 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a) {
     }
     if (in) {
       const uint8_t *p = static_cast<const uint8_t *>(a.x) + (row * a.ldx + c) * ES;
-      load8<DT>(p, x[u]);
-      if (GATED) load8<DT>(p + a.K * ES, up[u]);
+      load8<DT, FAR>(p, x[u]);
+      if (GATED) load8<DT, FAR>(p + a.K * ES, up[u]);
     }
   }
 #pragma unroll
@@ -156,7 +169,7 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a) {
     for (int d = 1; d < 16; d *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, d));
     const Scale k = block_scale(m);
     if (at[u] >= 0) {
-      *reinterpret_cast<u32x2_t *>(a.codes + at[u]) = codes8(x[u], k);
+      store8(a.codes + at[u], x[u], k);
       if (l == 0) a.scales[first + u * (kThreads / 16)] = k.s;
     }
   }
@@ -172,8 +185,8 @@ struct WeightArgs {
 
 // A workgroup has one block: 16 rows at a time, sixteen lanes to a row, the
 // whole block in registers between the maximum and the codes. Bound by HBM:
-// 17408 x 5120 of BF16, 267 MB, take 55 us (4.8 TB/s).
-template <int DT>
+// 17408 x 5120 of BF16, 267 MB, take 51 us (5.3 TB/s).
+template <int DT, bool FAR>
 __global__ __launch_bounds__(kThreads) void weight_kernel(WeightArgs a) {
   constexpr int ES = DT == NVFP4_F32 ? 4 : 2;
   __shared__ uint32_t tops[kThreads / 64];
@@ -189,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void weight_kernel(WeightArgs a) {
     const int64_t r = r0 + 16 * i;
 #pragma unroll
     for (int j = 0; j < 8; j++) x[i][j] = 0.0f;
-    if (r < a.N && c < a.K) load8<DT>(src + r * a.ldw * ES, x[i]);
+    if (r < a.N && c < a.K) load8<DT, FAR>(src + r * a.ldw * ES, x[i]);
   }
 #pragma unroll
   for (int i = 0; i < 8; i++) m = max(m, max8(x[i]));
@@ -204,11 +217,12 @@ __global__ __launch_bounds__(kThreads) void weight_kernel(WeightArgs a) {
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     const int64_t r = r0 + 16 * i;
-    if (r < a.N && c < a.K) *reinterpret_cast<u32x2_t *>(dst + r * a.K) = codes8(x[i], k);
+    if (r < a.N && c < a.K) store8(dst + r * a.K, x[i], k);
   }
   if (threadIdx.x == 0) a.scales[b] = k.s;
 }
 
+static int64_t element_bytes(int dtype) { return dtype == NVFP4_F32 ? 4 : 2; }
 static bool dtype_ok(int dtype) { return dtype == NVFP4_F32 || dtype == NVFP4_BF16 || dtype == NVFP4_F16; }
 
 }  // namespace fp8
@@ -216,6 +230,13 @@ static bool dtype_ok(int dtype) { return dtype == NVFP4_F32 || dtype == NVFP4_BF
 
 using namespace nvfp4;
 using namespace nvfp4::fp8;
+
+#define FP8_DISPATCH(dtype, far, CALL)                                                                \
+  switch (dtype) {                                                                                    \
+    case NVFP4_F32: if (far) { CALL(NVFP4_F32, true); } else { CALL(NVFP4_F32, false); } break;        \
+    case NVFP4_BF16: if (far) { CALL(NVFP4_BF16, true); } else { CALL(NVFP4_BF16, false); } break;     \
+    default: if (far) { CALL(NVFP4_F16, true); } else { CALL(NVFP4_F16, false); } break;               \
+  }
 
 extern "C" nvfp4_status nvfp4_fp8_quantize(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, int gated,
                                            uint8_t *codes, float *scales, void *stream) {
@@ -226,7 +247,7 @@ extern "C" nvfp4_status nvfp4_fp8_quantize(const void *x, int dtype, int64_t row
     return NVFP4_ERR_SHAPE;
   if (rows == 0) return NVFP4_OK;
   if (!x || !codes || !scales) return NVFP4_ERR_NULL;
-  if (!aligned(x, dtype == NVFP4_F32 ? 4 : 2) || !aligned(codes, 16) || !aligned(scales, 4)) return NVFP4_ERR_ALIGN;
+  if (!aligned(x, element_bytes(dtype)) || !aligned(codes, 16) || !aligned(scales, 4)) return NVFP4_ERR_ALIGN;
   RowsArgs a;
   a.x = x;
   a.ldx = ldx;
@@ -235,21 +256,17 @@ extern "C" nvfp4_status nvfp4_fp8_quantize(const void *x, int dtype, int64_t row
   a.K = K;
   a.codes = codes;
   a.scales = scales;
-  constexpr int U = 2;
-  const int64_t grid = (a.units + kThreads / 16 * U - 1) / (kThreads / 16 * U);
+  const int64_t grid = (a.units + kThreads / 16 * kRowBlocks - 1) / (kThreads / 16 * kRowBlocks);
   if (grid > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
   nvfp4_status st = device_info(nullptr);
   if (st != NVFP4_OK) return st;
-#define ROWS(DT)                                                                                                       \
-  if (gated)                                                                                                           \
-    hipLaunchKernelGGL((rows_kernel<DT, true, U>), dim3((unsigned)grid), dim3(kThreads), 0, (hipStream_t)stream, a);   \
-  else                                                                                                                 \
-    hipLaunchKernelGGL((rows_kernel<DT, false, U>), dim3((unsigned)grid), dim3(kThreads), 0, (hipStream_t)stream, a)
-  switch (dtype) {
-    case NVFP4_F32: ROWS(NVFP4_F32); break;
-    case NVFP4_BF16: ROWS(NVFP4_BF16); break;
-    default: ROWS(NVFP4_F16); break;
-  }
+  const bool far = rows * K * (gated ? 2 : 1) * element_bytes(dtype) > kNear;
+#define ROWS(DT, FAR)                                                                                                     \
+  if (gated)                                                                                                              \
+    hipLaunchKernelGGL((rows_kernel<DT, true, FAR>), dim3((unsigned)grid), dim3(kThreads), 0, (hipStream_t)stream, a);    \
+  else                                                                                                                    \
+    hipLaunchKernelGGL((rows_kernel<DT, false, FAR>), dim3((unsigned)grid), dim3(kThreads), 0, (hipStream_t)stream, a)
+  FP8_DISPATCH(dtype, far, ROWS)
 #undef ROWS
   NVFP4_LAUNCH_CHECK();
   return NVFP4_OK;
@@ -264,7 +281,7 @@ extern "C" nvfp4_status nvfp4_fp8_quantize_weight(const void *w, int dtype, int6
     return NVFP4_ERR_SHAPE;
   if (experts == 0) return NVFP4_OK;
   if (!w || !codes || !scales) return NVFP4_ERR_NULL;
-  if (!aligned(w, dtype == NVFP4_F32 ? 4 : 2) || !aligned(codes, 16) || !aligned(scales, 4)) return NVFP4_ERR_ALIGN;
+  if (!aligned(w, element_bytes(dtype)) || !aligned(codes, 16) || !aligned(scales, 4)) return NVFP4_ERR_ALIGN;
   WeightArgs a;
   a.w = w;
   a.ldw = ldw;
@@ -280,16 +297,11 @@ extern "C" nvfp4_status nvfp4_fp8_quantize_weight(const void *w, int dtype, int6
   const unsigned grid = (unsigned)(per * experts);
   nvfp4_status st = device_info(nullptr);
   if (st != NVFP4_OK) return st;
-  switch (dtype) {
-    case NVFP4_F32:
-      hipLaunchKernelGGL((weight_kernel<NVFP4_F32>), dim3(grid), dim3(kThreads), 0, (hipStream_t)stream, a);
-      break;
-    case NVFP4_BF16:
-      hipLaunchKernelGGL((weight_kernel<NVFP4_BF16>), dim3(grid), dim3(kThreads), 0, (hipStream_t)stream, a);
-      break;
-    default:
-      hipLaunchKernelGGL((weight_kernel<NVFP4_F16>), dim3(grid), dim3(kThreads), 0, (hipStream_t)stream, a);
-  }
+  const bool far = experts * N * K * element_bytes(dtype) > kNear;
+#define WEIGHT(DT, FAR) \
+  hipLaunchKernelGGL((weight_kernel<DT, FAR>), dim3(grid), dim3(kThreads), 0, (hipStream_t)stream, a)
+  FP8_DISPATCH(dtype, far, WEIGHT)
+#undef WEIGHT
   NVFP4_LAUNCH_CHECK();
   return NVFP4_OK;
 }

@@ -186,3 +186,19 @@ def test_captured_products_replayed_between_others(M, N, K):
         torch.cuda.synchronize()
         want = bf16(fp8.product(*c)[0])
         assert torch.equal(got.cpu(), want) and torch.equal(eager.cpu(), want)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16, torch.float32])
+def test_quantizers_of_inputs_past_the_caches(kind):
+    """Over 64 MB in all: rows of a wider matrix, gated rows and a weight give what parts of them, each under 64 MB, do."""
+    g = torch.Generator("cuda").manual_seed(3)
+    x = torch.randn((4400, 8 * 1040 + 8), generator=g, device="cuda").to(kind)[:, :8 * 1040]
+    for gated in (False, True):
+        codes, scales = nv.nvfp4_fp8_quantize(x, gated=gated)
+        for at in range(0, 4400, 400):
+            c, s = nv.nvfp4_fp8_quantize(x[at:at + 400], gated=gated)
+            assert torch.equal(codes[at:at + 400].view(torch.uint8), c.view(torch.uint8)) and torch.equal(scales[at:at + 400], s)
+    codes, scales = nv.nvfp4_fp8_quantize_weight(x)
+    for at in range(0, 4400, 384):
+        c, s = nv.nvfp4_fp8_quantize_weight(x[at:at + 384])
+        assert torch.equal(codes[at:at + 384].view(torch.uint8), c.view(torch.uint8)) and torch.equal(scales[at // 128:at // 128 + 3], s)
