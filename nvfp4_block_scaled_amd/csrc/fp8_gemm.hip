@@ -56,9 +56,14 @@ struct GemmArgs {
 // register between, from a buffer whose end the hardware checks: past it, zeros
 // arrive. The compiler does not see these loads: every reader waits for vmcnt
 // and passes a barrier first.
+template <bool ONCE>
 __device__ __forceinline__ void to_lds16(u32x4_t buf, uint32_t off, uint32_t lds, int plus) {
-  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(buf), "i"(plus)
-               : "m0", "scc", "memory");
+  if constexpr (ONCE)
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(lds), "v"(off), "s"(buf), "i"(plus)
+                 : "m0", "scc", "memory");
+  else
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(buf), "i"(plus)
+                 : "m0", "scc", "memory");
 }
 // Only when `skip` is 0 (a branch that the compiler does not see: one of its
 // own would part the step that it schedules as a whole).
@@ -205,7 +210,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // for one of 5120 x 17408. Between: the loads to LDS; without products and
 // fragments 256 x 2048 x 16400 takes 113 us of 118 in 128 x 128 tiles, 56 of 57
 // in 64 x 64.
-template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, bool SPLIT, bool F16>
+template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, bool SPLIT, bool ONCE, bool F16>
 __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(GemmArgs p) {
   constexpr int WAVES = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
   constexpr int LA = BM / 8 / WAVES, LW = BN / 8 / WAVES;                 // loads of a wave for a block
@@ -311,10 +316,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(GemmArgs p) {
     const uint32_t to = base + (vb & (STAGES - 1)) * STAGE;
     const u32x4_t bw = buffer(m.w, m.w_left, k0), ba = buffer(m.a, m.a_left, k0);
 #pragma unroll
-    for (int i = 0; i < LW; i++) to_lds16(bw, off_w[i], to + wave * LW * 1024, BM * 128 + i * 1024);
+    for (int i = 0; i < LW; i++) to_lds16<ONCE>(bw, off_w[i], to + wave * LW * 1024, BM * 128 + i * 1024);
     const bool had = kb == m.last && unit < from;
 #pragma unroll
-    for (int i = 0; i < LA; i++) to_lds16(ba, had ? kPastEnd : off_a[i], to + wave * LA * 1024, i * 1024);
+    for (int i = 0; i < LA; i++) to_lds16<false>(ba, had ? kPastEnd : off_a[i], to + wave * LA * 1024, i * 1024);
     const u32x4_t bs = buffer(m.s, m.s_left, (uint32_t)kb * 4);
 #pragma unroll
     for (int i = 0; i < LS; i++)       // with every fourth block, the rows' scales of four: [row][4]
@@ -621,7 +626,7 @@ __global__ __launch_bounds__(256) void add_parts_kernel(GemmArgs p) {
   }
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, bool SPLIT = false>
+template <int BM, int BN, int WM, int WN, int STAGES, bool GROUPED, bool SPLIT = false, bool ONCE = false>
 static nvfp4_status launch_tiles(GemmArgs a, int dtype, int per_cu, hipStream_t s) {
   a.tiles_n = (int32_t)((a.N + BN - 1) / BN);
   // grouped: at most, every expert ending in a partial tile
@@ -632,9 +637,9 @@ static nvfp4_status launch_tiles(GemmArgs a, int dtype, int per_cu, hipStream_t 
   const int64_t room = std::max(8, device_cus_or_default() / 8 * 8) * (int64_t)per_cu;
   const unsigned grid = (unsigned)std::min(room, (tiles + 7) / 8 * 8);
   if (dtype == NVFP4_F16)
-    hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, STAGES, GROUPED, SPLIT, true>), dim3(grid), dim3(64 * WM * WN), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, STAGES, GROUPED, SPLIT, ONCE, true>), dim3(grid), dim3(64 * WM * WN), 0, s, a);
   else
-    hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, STAGES, GROUPED, SPLIT, false>), dim3(grid), dim3(64 * WM * WN), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<BM, BN, WM, WN, STAGES, GROUPED, SPLIT, ONCE, false>), dim3(grid), dim3(64 * WM * WN), 0, s, a);
   NVFP4_LAUNCH_CHECK();
   if constexpr (SPLIT) {
     const unsigned adds = (unsigned)((a.M * ((a.N + 3) / 4) + 255) / 256);
@@ -735,11 +740,20 @@ static size_t parts_bytes(int64_t M, int64_t N, int parts) {
   return parts > 1 ? (size_t)parts * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4 : 0;
 }
 
+// ONCE: the rows are one tile, or, by expert, half of one on the average, so that
+// weights are read once and pass the caches by (nontemporal): 64 experts of 2560 x
+// 5120 and 256 rows 146 -> 135 us, 61 rows on 5120 x 17408 26.9 -> 25.6. Read again
+// by other rows' tiles they have to stay: 512 rows on 5120 x 5120 36.8 -> 47.
 static nvfp4_status launch_dense(GemmArgs a, int dtype, Plan plan, hipStream_t s) {
   a.parts = plan.parts;
-  if (plan.shape == 1)
-    return plan.parts > 1 ? launch_tiles<64, 64, 2, 2, 4, false, true>(a, dtype, kShapes[1].per_cu, s)
-                          : launch_tiles<64, 64, 2, 2, 4, false>(a, dtype, kShapes[1].per_cu, s);
+  if (plan.shape == 1) {
+    const int pc = kShapes[1].per_cu;
+    if (a.M <= 64)
+      return plan.parts > 1 ? launch_tiles<64, 64, 2, 2, 4, false, true, true>(a, dtype, pc, s)
+                            : launch_tiles<64, 64, 2, 2, 4, false, false, true>(a, dtype, pc, s);
+    return plan.parts > 1 ? launch_tiles<64, 64, 2, 2, 4, false, true>(a, dtype, pc, s)
+                          : launch_tiles<64, 64, 2, 2, 4, false>(a, dtype, pc, s);
+  }
   if (plan.shape == 2) return launch_tiles<64, 128, 2, 2, 2, false>(a, dtype, kShapes[2].per_cu, s);
   if (plan.shape == 3)
     return plan.parts > 1 ? launch_tiles<128, 128, 2, 2, 2, false, true>(a, dtype, kShapes[3].per_cu, s)
@@ -750,8 +764,13 @@ static nvfp4_status launch_dense(GemmArgs a, int dtype, Plan plan, hipStream_t s
 
 static nvfp4_status launch_grouped(GemmArgs a, int dtype, Plan plan, hipStream_t s) {
   a.parts = 1;
-  if (plan.shape == 0) return launch_tiles<32, 128, 1, 4, 4, true>(a, dtype, kShapes[0].per_cu, s);
-  if (plan.shape == 1) return launch_tiles<64, 64, 2, 2, 4, true>(a, dtype, kShapes[1].per_cu, s);
+  const bool once = plan.shape >= 0 && a.M <= (int64_t)a.experts * kShapes[plan.shape].bm / 2;
+  if (plan.shape == 0)
+    return once ? launch_tiles<32, 128, 1, 4, 4, true, false, true>(a, dtype, kShapes[0].per_cu, s)
+                : launch_tiles<32, 128, 1, 4, 4, true>(a, dtype, kShapes[0].per_cu, s);
+  if (plan.shape == 1)
+    return once ? launch_tiles<64, 64, 2, 2, 4, true, false, true>(a, dtype, kShapes[1].per_cu, s)
+                : launch_tiles<64, 64, 2, 2, 4, true>(a, dtype, kShapes[1].per_cu, s);
   if (plan.shape == 2) return launch_tiles<64, 128, 2, 2, 2, true>(a, dtype, kShapes[2].per_cu, s);
   if (plan.shape == 4) return launch_tiles<256, 256, 2, 4, 2, true>(a, dtype, kShapes[4].per_cu, s);
   return launch_stream<true>(a, dtype, s);
