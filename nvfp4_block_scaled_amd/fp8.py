@@ -34,6 +34,8 @@ def _matrix(t, name):
     """A [rows][cols] input with contiguous rows that do not overlap (copied once if it has none):
     (tensor kept alive, row stride)."""
     rows, cols = t.shape
+    if t.is_contiguous():
+        return t, cols
     if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
         t = t.clone(memory_format=torch.contiguous_format)
     return t, t.stride(0) if rows > 1 else cols
@@ -51,18 +53,18 @@ def _rows_out(out, name, dev, rows, cols, dtype):
     return out.stride(0) if rows > 1 else cols
 
 
-def _code_out(t, name, dev, shape, device):
+def _code_out(t, name, dev, shape, like):
     if t is None:
-        t = torch.empty(shape, dtype=torch.float8_e4m3fn, device=device)
+        t = like.new_empty(shape, dtype=torch.float8_e4m3fn)
         return t, t.data_ptr()
     if isinstance(t, torch.Tensor) and t.dtype == torch.uint8:
         return t, _flat(t, name, dev, torch.uint8, shape)
     return t, _flat(t, name, dev, torch.float8_e4m3fn, shape)
 
 
-def _scale_out(t, name, dev, shape, device):
+def _scale_out(t, name, dev, shape, like):
     if t is None:
-        t = torch.empty(shape, dtype=torch.float32, device=device)
+        t = like.new_empty(shape, dtype=torch.float32)
         return t, t.data_ptr()
     return t, _flat(t, name, dev, torch.float32, shape)
 
@@ -83,8 +85,8 @@ def nvfp4_fp8_quantize(x, gated=False, codes=None, scales=None):
     if K < 1 or K % 16:
         raise ValueError("K % 16 == 0 is required")
     x, ld = _matrix(x, "x")
-    codes, codes_at = _code_out(codes, "codes", dev, (M, K), x.device)
-    scales, scales_at = _scale_out(scales, "scales", dev, (M, _blocks(K)), x.device)
+    codes, codes_at = _code_out(codes, "codes", dev, (M, K), x)
+    scales, scales_at = _scale_out(scales, "scales", dev, (M, _blocks(K)), x)
     _check(lib().nvfp4_fp8_quantize(x.data_ptr(), kind, M, K, ld, 1 if gated else 0, codes_at, scales_at, _stream(dev)))
     return codes, scales
 
@@ -107,8 +109,8 @@ def nvfp4_fp8_quantize_weight(w, codes=None, scales=None):
     ld = ld if N > 1 else K
     es = es if E > 1 else 0
     lead = tuple(w.shape[:-2])
-    codes, codes_at = _code_out(codes, "codes", dev, lead + (N, K), w.device)
-    scales, scales_at = _scale_out(scales, "scales", dev, lead + (_blocks(N), _blocks(K)), w.device)
+    codes, codes_at = _code_out(codes, "codes", dev, lead + (N, K), w)
+    scales, scales_at = _scale_out(scales, "scales", dev, lead + (_blocks(N), _blocks(K)), w)
     _check(lib().nvfp4_fp8_quantize_weight(w.data_ptr(), kind, E, N, K, ld, es, codes_at, scales_at, _stream(dev)))
     return codes, scales
 
@@ -129,12 +131,12 @@ def _fp8(codes, scales, name, dev, dims, tall):
     return codes.data_ptr(), _flat(scales, name + "_scales", dev, torch.float32, shape)
 
 
-def _out(out, out_dtype, dev, M, N, device):
+def _out(out, out_dtype, dev, M, N, like):
     if out_dtype not in _OUT:
         raise TypeError("out_dtype must be 'bf16' or 'f16'")
     dtype = _OUT[out_dtype]
     if out is None:
-        return torch.empty((M, N), dtype=dtype, device=device), N, _DTYPES[dtype]
+        return like.new_empty((M, N), dtype=dtype), N, _DTYPES[dtype]
     return out, _rows_out(out, "out", dev, M, N, dtype), _DTYPES[dtype]
 
 
@@ -157,7 +159,7 @@ def nvfp4_fp8_gemm(a, a_scales, w, w_scales, out_dtype="bf16", out=None, ws=None
         raise ValueError(f"a has {K} columns, w {w.shape[1]}")
     if N < 1:
         raise ValueError("w has no rows")
-    out, ld, kind = _out(out, out_dtype, dev, M, N, a.device)
+    out, ld, kind = _out(out, out_dtype, dev, M, N, a)
     ws, wsp, nws = _bytes(ws, lib().nvfp4_fp8_gemm_workspace_bytes(M, N, K), dev)
     _check(lib().nvfp4_fp8_gemm(a_at, as_at, w_at, ws_at, M, N, K, out.data_ptr(), kind, ld, wsp, nws, _stream(dev)))
     return out
@@ -185,7 +187,7 @@ def nvfp4_fp8_gemm_grouped(a, a_scales, w, w_scales, offsets, rows=None, out_dty
             raise TypeError("rows must be a CUDA (HIP) tensor of one dimension")
         M = rows.shape[0]
         rows_at = _flat(rows, "rows", dev, torch.int32, (M,))
-    out, ld, kind = _out(out, out_dtype, dev, M, N, a.device)
+    out, ld, kind = _out(out, out_dtype, dev, M, N, a)
     _check(lib().nvfp4_fp8_gemm_grouped(a_at, as_at, a.shape[0], rows_at, w_at, ws_at, E, offsets_at, M, N, K,
                                         out.data_ptr(), kind, ld, _stream(dev)))
     return out

@@ -31,9 +31,9 @@ def nvfp4_moe_sort(ids, experts, ws=None):
         raise ValueError("experts must be 1 .. 1024")
     ids = ids.contiguous()
     T, top = ids.shape
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
-    tokens = torch.empty(T * top, dtype=torch.int32, device=ids.device)
-    places = torch.empty((T, top), dtype=torch.int32, device=ids.device)
+    offsets = ids.new_empty(experts + 1, dtype=torch.int32)
+    tokens = ids.new_empty(T * top, dtype=torch.int32)
+    places = ids.new_empty((T, top), dtype=torch.int32)
     ws, wsp, nws = _bytes(ws, lib().nvfp4_moe_sort_workspace_bytes(T, top, experts), dev)
     _check(lib().nvfp4_moe_sort(ids.data_ptr(), _IDS[ids.dtype], T, top, experts, offsets.data_ptr(), tokens.data_ptr(),
                                 places.data_ptr(), wsp, nws, _stream(dev)))
@@ -42,17 +42,20 @@ def nvfp4_moe_sort(ids, experts, ws=None):
 
 def _places(places, dev):
     """(address, tokens, top)"""
-    if not isinstance(places, torch.Tensor) or places.dim() != 2 or places.shape[1] < 1:
+    shape = places.shape if isinstance(places, torch.Tensor) else ()
+    if len(shape) != 2 or shape[1] < 1:
         raise TypeError("places must be a CUDA (HIP) tensor [tokens][top]")
-    return (_flat(places, "places", dev, torch.int32, tuple(places.shape)),) + tuple(places.shape)
+    return _flat(places, "places", dev, torch.int32, shape), shape[0], shape[1]
 
 
 def _input(t, name, dev, rows):
+    """(tensor kept alive, its dtype's code, row stride, columns)"""
     kind = _floats(t, name, dev)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < 1:
-        raise ValueError(f"{name} must be [{rows}][>= 1], got {list(t.shape)}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] < 1:
+        raise ValueError(f"{name} must be [{rows}][>= 1], got {list(shape)}")
     t, ld = _matrix(t, name)
-    return t, kind, ld
+    return t, kind, ld, shape[1]
 
 
 def _apart(out, name, *inputs):
@@ -72,7 +75,7 @@ def _span(t):
 
 def _output(out, name, dev, rows, width, like, *inputs):
     if out is None:
-        return torch.empty((rows, width), dtype=like.dtype, device=like.device), width
+        return like.new_empty((rows, width)), width
     ld = _rows_out(out, name, dev, rows, width, like.dtype)
     _apart(out, name, *inputs)
     return out, ld
@@ -84,9 +87,9 @@ def nvfp4_moe_gather(x, places, out=None):
     (undefined in a new out)."""
     dev = _device()
     at, T, top = _places(places, dev)
-    x, kind, ldx = _input(x, "x", dev, T)
-    out, ldo = _output(out, "out", dev, T * top, x.shape[1], x, x)
-    _check(lib().nvfp4_moe_gather(x.data_ptr(), kind, ldx, at, T, top, x.shape[1], out.data_ptr(), ldo, _stream(dev)))
+    x, kind, ldx, width = _input(x, "x", dev, T)
+    out, ldo = _output(out, "out", dev, T * top, width, x, x)
+    _check(lib().nvfp4_moe_gather(x.data_ptr(), kind, ldx, at, T, top, width, out.data_ptr(), ldo, _stream(dev)))
     return out
 
 
@@ -99,11 +102,10 @@ def nvfp4_moe_combine(y, places, weights=None, out=None):
     (weights float32 [T][top]; None: ones), summed in FP32 in the order of j and rounded once."""
     dev = _device()
     at, T, top = _places(places, dev)
-    y, kind, ldy = _input(y, "y", dev, T * top)
+    y, kind, ldy, width = _input(y, "y", dev, T * top)
     w_at = None if weights is None else _weights(weights, dev, T, top)
-    out, ldo = _output(out, "out", dev, T, y.shape[1], y, y)
-    _check(lib().nvfp4_moe_combine(y.data_ptr(), kind, ldy, at, w_at, T, top, y.shape[1], out.data_ptr(), ldo,
-                                   _stream(dev)))
+    out, ldo = _output(out, "out", dev, T, width, y, y)
+    _check(lib().nvfp4_moe_combine(y.data_ptr(), kind, ldy, at, w_at, T, top, width, out.data_ptr(), ldo, _stream(dev)))
     return out
 
 
@@ -118,15 +120,15 @@ def nvfp4_moe_combine_backward(grad, y, places, weights, grad_y=None):
     of grad_y that no place names are left as they were (undefined in a new grad_y)."""
     dev = _device()
     at, T, top = _places(places, dev)
-    y, kind, ldy = _input(y, "y", dev, T * top)
-    grad, other, ldg = _input(grad, "grad", dev, T)
+    y, kind, ldy, width = _input(y, "y", dev, T * top)
+    grad, other, ldg, columns = _input(grad, "grad", dev, T)
     if other != kind:
         raise TypeError("grad and y must have one type")
-    if grad.shape[1] != y.shape[1]:
-        raise ValueError(f"grad has {grad.shape[1]} columns, y {y.shape[1]}")
+    if columns != width:
+        raise ValueError(f"grad has {columns} columns, y {width}")
     w_at = _weights(weights, dev, T, top)
-    grad_y, ldo = _output(grad_y, "grad_y", dev, T * top, y.shape[1], y, y, grad)
-    grad_weights = torch.empty((T, top), dtype=torch.float32, device=y.device)
-    _check(lib().nvfp4_moe_combine_backward(grad.data_ptr(), ldg, y.data_ptr(), ldy, kind, at, w_at, T, top, y.shape[1],
+    grad_y, ldo = _output(grad_y, "grad_y", dev, T * top, width, y, y, grad)
+    grad_weights = y.new_empty((T, top), dtype=torch.float32)
+    _check(lib().nvfp4_moe_combine_backward(grad.data_ptr(), ldg, y.data_ptr(), ldy, kind, at, w_at, T, top, width,
                                             grad_y.data_ptr(), ldo, grad_weights.data_ptr(), _stream(dev)))
     return grad_y, grad_weights
