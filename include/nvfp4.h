@@ -523,7 +523,8 @@ nvfp4_status nvfp4_kv_compact(const nvfp4_kv_pool *pool, const int32_t *table, i
  * consecutive values of a row, [M][ceil(K/128)]; a weight [N][K] one for each
  * 128 x 128 block, [ceil(N/128)][ceil(K/128)]. Codes are row-major bytes, rows
  * K bytes apart, 16-byte aligned; K % 16 == 0. Nothing is prepared or laid out
- * anew: the products read the codes as they are. */
+ * anew: the products read the codes as they are. Outputs and workspaces lie
+ * apart from inputs, and from one another. */
 
 /* BF16, FP16 or FP32 rows -> FP8 rows.
  *  x      [rows][K] of dtype (nvfp4_dtype), rows ldx elements apart; with gated,

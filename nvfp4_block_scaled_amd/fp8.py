@@ -53,20 +53,38 @@ def _rows_out(out, name, dev, rows, cols, dtype):
     return out.stride(0) if rows > 1 else cols
 
 
+def _span(t):
+    """Bytes from a tensor's first element to its last."""
+    if t.numel() == 0:
+        return 0
+    return (sum((n - 1) * st for n, st in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
+def _apart(out, name, *inputs):
+    """An output must not share storage with an input in the bytes that both cover."""
+    lo, hi = out.data_ptr(), out.data_ptr() + _span(out)
+    for t in inputs:
+        if t.data_ptr() < hi and lo < t.data_ptr() + _span(t):
+            raise ValueError(f"{name} overlaps an input")
+
+
 def _code_out(t, name, dev, shape, like):
     if t is None:
         t = like.new_empty(shape, dtype=torch.float8_e4m3fn)
         return t, t.data_ptr()
-    if isinstance(t, torch.Tensor) and t.dtype == torch.uint8:
-        return t, _flat(t, name, dev, torch.uint8, shape)
-    return t, _flat(t, name, dev, torch.float8_e4m3fn, shape)
+    as_bytes = isinstance(t, torch.Tensor) and t.dtype == torch.uint8
+    at = _flat(t, name, dev, torch.uint8 if as_bytes else torch.float8_e4m3fn, shape)
+    _apart(t, name, like)
+    return t, at
 
 
 def _scale_out(t, name, dev, shape, like):
     if t is None:
         t = like.new_empty(shape, dtype=torch.float32)
         return t, t.data_ptr()
-    return t, _flat(t, name, dev, torch.float32, shape)
+    at = _flat(t, name, dev, torch.float32, shape)
+    _apart(t, name, like)
+    return t, at
 
 
 def nvfp4_fp8_quantize(x, gated=False, codes=None, scales=None):
@@ -131,13 +149,15 @@ def _fp8(codes, scales, name, dev, dims, tall):
     return codes.data_ptr(), _flat(scales, name + "_scales", dev, torch.float32, shape)
 
 
-def _out(out, out_dtype, dev, M, N, like):
+def _out(out, out_dtype, dev, M, N, *inputs):
     if out_dtype not in _OUT:
         raise TypeError("out_dtype must be 'bf16' or 'f16'")
     dtype = _OUT[out_dtype]
     if out is None:
-        return like.new_empty((M, N), dtype=dtype), N, _DTYPES[dtype]
-    return out, _rows_out(out, "out", dev, M, N, dtype), _DTYPES[dtype]
+        return inputs[0].new_empty((M, N), dtype=dtype), N, _DTYPES[dtype]
+    ld = _rows_out(out, "out", dev, M, N, dtype)
+    _apart(out, "out", *inputs)
+    return out, ld, _DTYPES[dtype]
 
 
 def nvfp4_fp8_gemm_workspace(M, N, K):
@@ -159,7 +179,7 @@ def nvfp4_fp8_gemm(a, a_scales, w, w_scales, out_dtype="bf16", out=None, ws=None
         raise ValueError(f"a has {K} columns, w {w.shape[1]}")
     if N < 1:
         raise ValueError("w has no rows")
-    out, ld, kind = _out(out, out_dtype, dev, M, N, a)
+    out, ld, kind = _out(out, out_dtype, dev, M, N, a, a_scales, w, w_scales)
     ws, wsp, nws = _bytes(ws, lib().nvfp4_fp8_gemm_workspace_bytes(M, N, K), dev)
     _check(lib().nvfp4_fp8_gemm(a_at, as_at, w_at, ws_at, M, N, K, out.data_ptr(), kind, ld, wsp, nws, _stream(dev)))
     return out
@@ -187,7 +207,7 @@ def nvfp4_fp8_gemm_grouped(a, a_scales, w, w_scales, offsets, rows=None, out_dty
             raise TypeError("rows must be a CUDA (HIP) tensor of one dimension")
         M = rows.shape[0]
         rows_at = _flat(rows, "rows", dev, torch.int32, (M,))
-    out, ld, kind = _out(out, out_dtype, dev, M, N, a)
+    out, ld, kind = _out(out, out_dtype, dev, M, N, a, a_scales, w, w_scales, offsets, *(() if rows is None else (rows,)))
     _check(lib().nvfp4_fp8_gemm_grouped(a_at, as_at, a.shape[0], rows_at, w_at, ws_at, E, offsets_at, M, N, K,
                                         out.data_ptr(), kind, ld, _stream(dev)))
     return out

@@ -11,7 +11,7 @@ range stands for no row.
 import torch
 
 from . import _check, lib
-from .fp8 import _floats, _matrix, _rows_out
+from .fp8 import _apart, _floats, _matrix, _rows_out
 from .kv_cache import _at, _bytes, _device, _flat, _stream
 
 _IDS = {torch.int32: 4, torch.int64: 8}
@@ -56,21 +56,6 @@ def _input(t, name, dev, rows):
         raise ValueError(f"{name} must be [{rows}][>= 1], got {list(shape)}")
     t, ld = _matrix(t, name)
     return t, kind, ld, shape[1]
-
-
-def _apart(out, name, *inputs):
-    """An output must not share storage with an input in the bytes that both cover."""
-    lo, hi = out.data_ptr(), out.data_ptr() + _span(out)
-    for t in inputs:
-        if t.data_ptr() < hi and lo < t.data_ptr() + _span(t):
-            raise ValueError(f"{name} overlaps an input")
-
-
-def _span(t):
-    """Bytes from a matrix's first element to its last."""
-    if t.numel() == 0:
-        return 0
-    return ((t.shape[0] - 1) * t.stride(0) + (t.shape[1] - 1) * t.stride(1) + 1) * t.element_size()
 
 
 def _output(out, name, dev, rows, width, like, *inputs):

@@ -202,3 +202,33 @@ def test_quantizers_of_inputs_past_the_caches(kind):
     for at in range(0, 4400, 384):
         c, s = nv.nvfp4_fp8_quantize_weight(x[at:at + 384])
         assert torch.equal(codes[at:at + 384].view(torch.uint8), c.view(torch.uint8)) and torch.equal(scales[at // 128:at // 128 + 3], s)
+
+
+def test_outputs_over_inputs_are_refused():
+    """Every output that the caller gives, over every input; behind the input's last byte it may begin."""
+    room = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+
+    def at(first, shape, dtype):
+        n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+        return room[first:first + n].view(dtype).view(shape)
+    f8, f4, b2 = torch.float8_e4m3fn, torch.float32, torch.bfloat16
+    x, codes, scales = at(0, (4, 256), b2), at(2048, (4, 256), f8), at(4096, (4, 2), f4)
+    nv.nvfp4_fp8_quantize(x, codes=codes, scales=scales)
+    for bad in (dict(codes=at(2032, (4, 256), f8)), dict(scales=at(2044, (4, 2), f4)), dict(codes=at(0, (4, 256), torch.uint8))):
+        with pytest.raises(ValueError):
+            nv.nvfp4_fp8_quantize(x, **bad)
+    w, sw = at(8192, (16, 256), f8), at(16384, (1, 2), f4)
+    nv.nvfp4_fp8_quantize_weight(x, codes=codes, scales=at(4096, (1, 2), f4))
+    with pytest.raises(ValueError):
+        nv.nvfp4_fp8_quantize_weight(x, codes=at(1024, (4, 256), f8))
+    offsets, rows = at(20480, (2,), torch.int32), at(20496, (4,), torch.int32)
+    out = at(2048 - 128, (4, 16), b2)
+    nv.nvfp4_fp8_gemm(codes, scales, w, sw, out=out)
+    nv.nvfp4_fp8_gemm_grouped(codes, scales, w[None], sw[None], offsets, rows=rows, out=out)
+    for first in (2048 - 126, 2048 + 1022, 4096 + 30, 8192 + 4094, 16384 + 6):
+        with pytest.raises(ValueError):
+            nv.nvfp4_fp8_gemm(codes, scales, w, sw, out=at(first, (4, 16), b2))
+    for first in (2048, 20480 + 6, 20496 + 14):
+        with pytest.raises(ValueError):
+            nv.nvfp4_fp8_gemm_grouped(codes, scales, w[None], sw[None], offsets, rows=rows, out=at(first, (4, 16), b2))
+    torch.cuda.synchronize()
