@@ -26,9 +26,9 @@ constexpr uint32_t kInfBits = 0x7F800000u;
 
 // Inputs of over 64 MB (FAR) are read, and codes always written, past the caches
 // (nontemporal): a large input has mostly left them, and what it would push out
-// is worth more. Gated rows of 2 x 17408 BF16: 2048 38.9 -> 35.9 us, 8192 137 -> 130
-// (after a kernel that wrote them 248 -> 200); of inputs, 84 MB gain 8 % by it, 36
-// MB lose 3 to 7 %. Codes so written are read back by the next kernel as fast.
+// is worth more. A weight of 17408 x 5120 55 -> 50 us; 8192 gated rows of 2 x 17408
+// after a kernel that wrote them 248 -> 200; of inputs, 84 MB gain 8 % by it, 36 MB
+// lose 3 to 7 %. Codes so written are read back by the next kernel as fast.
 constexpr int64_t kNear = int64_t(64) << 20;
 
 template <bool FAR, typename U>
@@ -54,13 +54,20 @@ __device__ __forceinline__ void load8(const void *p, float (&x)[8]) {
   }
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
+// The largest |x| of eight as bits; a NaN if one is there (v_maximum3 keeps it).
 __device__ __forceinline__ uint32_t max8(const float (&x)[8]) {
-  uint32_t m = 0;
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; i++) m = max(m, abs_bits(x[i]));
-  return m;
+  for (int i = 0; i < 8; i += 2) asm("v_maximum3_f32 %0, |%1|, |%2|, %0" : "+v"(m) : "v"(x[i]), "v"(x[i + 1]));
+  return __float_as_uint(m) & 0x7FFFFFFFu;
+}
+
+// The largest of 16 lanes' (a row of the cross-lane network, turned by 8, 4, 2, 1), in each of them.
+__device__ __forceinline__ uint32_t max16(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x128, 0xF, 0xF, false));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x124, 0xF, 0xF, false));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x122, 0xF, 0xF, false));
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x121, 0xF, 0xF, false));
 }
 
 // The scale of a block whose largest |x| has these bits, and its reciprocal.
@@ -78,10 +85,11 @@ __device__ __forceinline__ Scale block_scale(uint32_t top) {
   return k;
 }
 
-// RN(x / s) for |x| <= 448 s (or a NaN where s is one), a zero's sign kept.
+// RN(x / s) for |x| <= 448 s (or a NaN where s is one). With the remainder taken
+// from -x and negated, a remainder of zero is a zero of x's sign where x is one.
 __device__ __forceinline__ float quotient(float x, Scale k) {
   const float q = x * k.r;
-  return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q, k.s, x), k.r, q), x);
+  return __builtin_fmaf(-__builtin_fmaf(q, k.s, -x), k.r, q);
 }
 
 __device__ __forceinline__ void store8(uint8_t *to, const float (&x)[8], Scale k) {
@@ -100,8 +108,10 @@ __device__ __forceinline__ void store8(uint8_t *to, const float (&x)[8], Scale k
 // -87 .. 104 there: above, 1 + e^-g is 1; below, the result is under 2^-119
 // either way, less than the smallest scale. The reciprocal is good to an ulp and
 // the quotient, after one step with its remainder, to hardly more than half of
-// one. The arithmetic counts here: with the library's expf and a division by a
-// corrected reciprocal, 2048 rows of 2 x 17408 BF16 columns took 47.6 us, so 41.
+// one: off by 0.84 units of 2^-24 in the mean. The arithmetic counts here: 2048
+// rows of 2 x 17408 BF16 columns take 30 to 31 us, 47.6 with the library's expf, a
+// corrected reciprocal and a long division for each block's row; carrying what
+// the sum and the quotient lose into the product (0.54 units) would cost 5.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
   const float c = __builtin_amdgcn_fmed3f(g, -87.0f, 104.0f);
@@ -120,43 +130,43 @@ struct RowsArgs {
   int64_t units;         // rows * blocks of a row
   int64_t K;
   int32_t blocks;        // of a row
+  uint64_t inverse;      // 2^64 / blocks, rounded up (blocks > 1)
+  uint32_t small;        // 2^16 / blocks + 1
   uint8_t *codes;
   float *scales;
 };
 
-// Sixteen lanes have a block of 128 columns, eight columns each; a thread has U
-// blocks, whose loads are all in flight before the first is used (two: one, three
-// and four are 1 to 8 % slower). K % 16 == 0: a lane's eight columns are all
-// there or none is. Bound by HBM: 2048 rows of 34816 BF16 columns, 214 MB read
-// and written, take 39 us (5.5 TB/s); gated into 17408, 178 MB, 36 to 39 (4.6 and
-// more; the vector units are as busy then).
+// Sixteen lanes have a block of 128 columns, eight columns each; a thread has
+// kRowBlocks blocks, whose loads are all in flight before the first is used (two:
+// one, three and four are 1 to 8 % slower). K % 16 == 0: a lane's eight columns
+// are all there or none is. Bound by HBM: 2048 rows of 34816 BF16 columns, 214 MB
+// read and written, take 35 us (6.1 TB/s); gated into 17408, 178 MB, 30 to 31 (5.8).
 constexpr int kThreads = 256, kRowBlocks = 2;
 
 template <int DT, bool GATED, bool FAR>
 __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a) {
   constexpr int ES = DT == NVFP4_F32 ? 4 : 2, U = kRowBlocks;
-  const int l = threadIdx.x & 15;
-  const int64_t first = (int64_t)blockIdx.x * (kThreads / 16 * U) + (threadIdx.x >> 4);
+  const int l = threadIdx.x & 15, group = threadIdx.x >> 4;
+  // The row of the workgroup's first block by one long product on the scalar unit (exact: units times blocks stay below
+  // 2^64), its other blocks' from there: at most one row further, or by a short product where rows have few blocks.
+  const uint64_t unit0 = (uint64_t)blockIdx.x * (kThreads / 16 * U), row0 = a.blocks > 1 ? __umul64hi(unit0, a.inverse) : unit0;
+  const uint32_t block0 = (uint32_t)(unit0 - row0 * (uint32_t)a.blocks);
+  const uint8_t *src = static_cast<const uint8_t *>(a.x) + row0 * a.ldx * ES;
+  uint8_t *dst = a.codes + row0 * a.K;
   float x[U][8], up[GATED ? U : 1][8];
-  int64_t at[U];         // of the lane's columns in codes, or -1
+  uint64_t at[U];        // of the lane's columns in dst
+  bool in[U];
 #pragma unroll
   for (int u = 0; u < U; u++) {
-    const int64_t unit = first + u * (kThreads / 16);
-    const int64_t row = unit / a.blocks;
-    const int64_t c = (unit - row * a.blocks) * 128 + l * 8;
-    const bool in = unit < a.units && c < a.K;
-    at[u] = in ? row * a.K + c : -1;
-#pragma unroll
-    for (int i = 0; i < 8; i++) x[u][i] = 0.0f;
-    if (GATED) {
-#pragma unroll
-      for (int i = 0; i < 8; i++) up[u][i] = 0.0f;
-    }
-    if (in) {
-      const uint8_t *p = static_cast<const uint8_t *>(a.x) + (row * a.ldx + c) * ES;
-      load8<DT, FAR>(p, x[u]);
-      if (GATED) load8<DT, FAR>(p + a.K * ES, up[u]);
-    }
+    const uint32_t b = block0 + u * (kThreads / 16) + group;
+    const uint32_t down = a.blocks >= kThreads / 16 * U ? (uint32_t)(b >= (uint32_t)a.blocks) : (b * a.small) >> 16;
+    const uint32_t c = (b - down * (uint32_t)a.blocks) * 128 + l * 8;
+    in[u] = unit0 + u * (kThreads / 16) + group < (uint64_t)a.units && c < a.K;
+    at[u] = (uint64_t)down * (uint32_t)a.K + c;
+    // Lanes past the end or past the row's last column: eight columns that there are, which count as zeros.
+    const uint8_t *p = in[u] ? src + ((uint64_t)down * (uint32_t)a.ldx + c) * ES : static_cast<const uint8_t *>(a.x);
+    load8<DT, FAR>(p, x[u]);
+    if (GATED) load8<DT, FAR>(p + a.K * ES, up[u]);
   }
 #pragma unroll
   for (int u = 0; u < U; u++) {
@@ -164,13 +174,10 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; i++) x[u][i] = silu_mul(x[u][i], up[u][i]);
     }
-    uint32_t m = max8(x[u]);
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-    const Scale k = block_scale(m);
-    if (at[u] >= 0) {
-      store8(a.codes + at[u], x[u], k);
-      if (l == 0) a.scales[first + u * (kThreads / 16)] = k.s;
+    const Scale k = block_scale(max16(in[u] ? max8(x[u]) : 0));
+    if (in[u]) {
+      store8(dst + at[u], x[u], k);
+      if (l == 0) a.scales[unit0 + u * (kThreads / 16) + group] = k.s;
     }
   }
 }
@@ -185,7 +192,7 @@ struct WeightArgs {
 
 // A workgroup has one block: 16 rows at a time, sixteen lanes to a row, the
 // whole block in registers between the maximum and the codes. Bound by HBM:
-// 17408 x 5120 of BF16, 267 MB, take 51 us (5.3 TB/s).
+// 17408 x 5120 of BF16, 267 MB, take 50 us (5.3 TB/s).
 template <int DT, bool FAR>
 __global__ __launch_bounds__(kThreads) void weight_kernel(WeightArgs a) {
   constexpr int ES = DT == NVFP4_F32 ? 4 : 2;
@@ -253,6 +260,8 @@ extern "C" nvfp4_status nvfp4_fp8_quantize(const void *x, int dtype, int64_t row
   a.ldx = ldx;
   a.blocks = (int32_t)((K + 127) / 128);
   a.units = rows * a.blocks;
+  a.inverse = ~0ull / (uint64_t)a.blocks + 1;
+  a.small = (1u << 16) / (uint32_t)a.blocks + 1;
   a.K = K;
   a.codes = codes;
   a.scales = scales;

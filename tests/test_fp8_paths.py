@@ -232,3 +232,16 @@ def test_outputs_over_inputs_are_refused():
         with pytest.raises(ValueError):
             nv.nvfp4_fp8_gemm_grouped(codes, scales, w[None], sw[None], offsets, rows=rows, out=at(first, (4, 16), b2))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rows,K", [(33, 128), (70, 256), (41, 3968), (35, 4096), (9, 4112), (1, 16400), (1000, 16), (3, 100000)])
+def test_quantized_rows_across_workgroups(rows, K):
+    """Rows of 1, 2, 31, 32, 33 and many blocks, 32 blocks to a workgroup; zeros of both signs keep theirs."""
+    x = rng(K).standard_normal((rows, K)).astype(np.float32)
+    x[:, ::7] = 0.0
+    x[:, 3::11] = -0.0
+    x[rows // 2, K // 2:] = -0.0
+    codes, scales = nv.nvfp4_fp8_quantize(dev(x))
+    want_c, want_s = fp8.quantize(x)
+    np.testing.assert_array_equal(scales.cpu().numpy(), want_s)
+    np.testing.assert_array_equal(codes.view(torch.uint8).cpu().numpy(), want_c)
