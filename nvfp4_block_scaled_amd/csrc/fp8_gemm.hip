@@ -204,9 +204,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // last products. Eight waves of 128 x 64 leave 512 / 2 registers a lane: 128
 // sums, 48 of fragments, 32 of products under way.
 //
-// What bounds it. 256 x 256: 8192 x 17408 x 5120 take 663 .. 690 us (2150
+// What bounds it. 256 x 256: 8192 x 17408 x 5120 take 663 .. 702 us (2150
 // TFLOP/s), the matrix cores 55 % busy at a clock that the power holds at 1.7 to
-// 2.05 GHz. Weights for few rows: HBM, 6.1 TB/s for 64 experts of 2560 x 5120, 4.6
+// 2.05 GHz. Weights for few rows: HBM, 6.6 TB/s for 64 experts of 2560 x 5120, 4.3
 // for one of 5120 x 17408. Between: the loads to LDS; without products and
 // fragments 256 x 2048 x 16400 takes 113 us of 118 in 128 x 128 tiles, 56 of 57
 // in 64 x 64.
