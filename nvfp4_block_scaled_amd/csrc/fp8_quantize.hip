@@ -201,16 +201,12 @@ __global__ __launch_bounds__(kThreads) void weight_kernel(WeightArgs a) {
   const int64_t cb = b % a.blocks, rb = b / a.blocks % a.row_blocks, e = b / a.blocks / a.row_blocks;
   const int64_t c = cb * 128 + (threadIdx.x & 15) * 8;
   const int64_t r0 = rb * 128 + (threadIdx.x >> 4);
-  const uint8_t *src = static_cast<const uint8_t *>(a.w) + (e * a.expert_stride + c) * ES;
+  // Past the last row or column: that row, the last eight columns. They are the block's own and leave its maximum alone.
+  const uint8_t *src = static_cast<const uint8_t *>(a.w) + (e * a.expert_stride + min(c, a.K - 8)) * ES;
   float x[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) load8<DT, FAR>(src + min(r0 + 16 * i, a.N - 1) * a.ldw * ES, x[i]);
   uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const int64_t r = r0 + 16 * i;
-#pragma unroll
-    for (int j = 0; j < 8; j++) x[i][j] = 0.0f;
-    if (r < a.N && c < a.K) load8<DT, FAR>(src + r * a.ldw * ES, x[i]);
-  }
 #pragma unroll
   for (int i = 0; i < 8; i++) m = max(m, max8(x[i]));
 #pragma unroll
