@@ -106,22 +106,23 @@ __device__ __forceinline__ void store8(uint8_t *to, const float (&x)[8], Scale k
 // silu(g) u = g / (1 + e^-g) u. With t = RN(-g log2 e) and what that rounding
 // lost, l (exact but for 2^-48 of t), e^-g = 2^t (1 + l ln 2). g is taken within
 // -87 .. 104 there: above, 1 + e^-g is 1; below, the result is under 2^-119
-// either way, less than the smallest scale. The reciprocal is good to an ulp and
-// the quotient, after one step with its remainder, to hardly more than half of
-// one: off by 0.84 units of 2^-24 in the mean. The arithmetic counts here: 2048
-// rows of 2 x 17408 BF16 columns take 30 to 31 us, 47.6 with the library's expf, a
-// corrected reciprocal and a long division for each block's row; carrying what
-// the sum and the quotient lose into the product (0.54 units) would cost 5.
+// either way, less than the smallest scale. The quotient q by a reciprocal good to
+// an ulp has the remainder g - q - q e, where g - q is exact for g > 0 (q is half of
+// g at least), so the sum 1 + e need not be; remainder and q meet in the one
+// multiply-add that rounds the result. Scales are 3.7e-8 off in the mean; 5.5e-8,
+// and a quarter more codes on the other side of a tie, where the quotient is
+// rounded before it meets u. The arithmetic counts here: 2048 rows of 2 x 17408
+// BF16 columns take 32 us, two less without that, 47.6 with the library's expf, a
+// corrected reciprocal and a long division for each block's row.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
   const float c = __builtin_amdgcn_fmed3f(g, -87.0f, 104.0f);
   const float t = c * -kLog2e;
   const float l = __builtin_fmaf(c, -kLog2eRest, __builtin_fmaf(c, -kLog2e, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  const float d = 1.0f + __builtin_fmaf(e, l * kLn2, e);
-  const float r = __builtin_amdgcn_rcpf(d);
+  const float p = __builtin_amdgcn_exp2f(t), e = __builtin_fmaf(p, l * kLn2, p);
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
   const float q = g * r;
-  return __builtin_fmaf(__builtin_fmaf(-q, d, g), r, q) * u;
+  return __builtin_fmaf(q, u, __builtin_fmaf(-q, e, g - q) * r * u);
 }
 
 struct RowsArgs {
@@ -140,7 +141,7 @@ struct RowsArgs {
 // kRowBlocks blocks, whose loads are all in flight before the first is used (two:
 // one, three and four are 1 to 8 % slower). K % 16 == 0: a lane's eight columns
 // are all there or none is. Bound by HBM: 2048 rows of 34816 BF16 columns, 214 MB
-// read and written, take 35 us (6.1 TB/s); gated into 17408, 178 MB, 30 to 31 (5.8).
+// read and written, take 35 us (6.1 TB/s); gated into 17408, 178 MB, 32 (5.6).
 constexpr int kThreads = 256, kRowBlocks = 2;
 
 template <int DT, bool GATED, bool FAR>

@@ -86,7 +86,7 @@ def test_quantize_rows(rows, cols, pad, kind):
 @pytest.mark.parametrize("rows,cols,pad", [(1, 16, 0), (2, 128, 0), (33, 1040, 8), (300, 272, 3)])
 def test_quantize_gated_rows(rows, cols, pad, kind):
     """silu(g) u in FP32 is off by a few units of 2^-24: e^-g by three (2^t by an ulp, its correction by half of one), the
-    sum by one, the corrected quotient by one and a little, the product by one: under 2^-21 of the value. The scale then is
+    sum by one, the reciprocal by little after the remainder, the product by one: under 2^-21 of the value. The scale then is
     off by that and its own half step, and a code's value by half a step of E4M3 (2^-4 of the value, at least 2^-10 of a
     scale) and that."""
     r = rng(rows * cols)
