@@ -529,7 +529,8 @@ nvfp4_status nvfp4_kv_compact(const nvfp4_kv_pool *pool, const int32_t *table, i
 /* BF16, FP16 or FP32 rows -> FP8 rows.
  *  x      [rows][K] of dtype (nvfp4_dtype), rows ldx elements apart; with gated,
  *         [rows][2K]: columns 0 .. K-1 are a gate g, K .. 2K-1 a factor u, and
- *         silu(g) u = g / (1 + e^-g) u, in FP32, is quantized.
+ *         silu(g) u = g / (1 + e^-g) u, within 2^-21 of its value or 2^-110, is
+ *         quantized: a gate masked with a type's lowest value gives 0.
  *  scale  max(amax, 2^-100) / 448 of the block, one IEEE FP32 division; code
  *         E4M3_RNE(x / scale), the quotient rounded to FP32 first. A block with
  *         a NaN or an infinity gets scale NaN and NaN codes.

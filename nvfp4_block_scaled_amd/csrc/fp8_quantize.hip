@@ -103,26 +103,42 @@ __device__ __forceinline__ void store8(uint8_t *to, const float (&x)[8], Scale k
   __builtin_nontemporal_store(c, reinterpret_cast<u32x2_t *>(to));
 }
 
-// silu(g) u = g / (1 + e^-g) u. With t = RN(-g log2 e) and what that rounding
-// lost, l (exact but for 2^-48 of t), e^-g = 2^t (1 + l ln 2). g is taken within
-// -87 .. 104 there: above, 1 + e^-g is 1; below, the result is under 2^-119
-// either way, less than the smallest scale. The quotient q by a reciprocal good to
-// an ulp has the remainder g - q - q e, where g - q is exact for g > 0 (q is half of
-// g at least), so the sum 1 + e need not be; remainder and q meet in the one
-// multiply-add that rounds the result. Scales are 3.7e-8 off in the mean; 5.5e-8,
-// and a quarter more codes on the other side of a tie, where the quotient is
-// rounded before it meets u. The arithmetic counts here: 2048 rows of 2 x 17408
-// BF16 columns take 32 us, two less without that, 47.6 with the library's expf, a
-// corrected reciprocal and a long division for each block's row.
+// silu(g) u = g / (1 + e^-g) u for |g| <= 87. With t = RN(-g log2 e) and what that
+// rounding lost, l (exact but for 2^-48 of t), e^-g = 2^t (1 + l ln 2), which is
+// below 2^126, so the reciprocal of 1 + e^-g is a normal number. The quotient q by
+// a reciprocal good to an ulp has the remainder g - q - q e, where g - q is exact
+// for g > 0 (q is half of g at least), so the sum 1 + e need not be; remainder and
+// q meet in the one multiply-add that rounds the result. Scales are 3.7e-8 off in
+// the mean; 5.5e-8, and a quarter more codes on the other side of a tie, where the
+// quotient is rounded before it meets u. The arithmetic counts here: 2048 rows of
+// 2 x 17408 BF16 columns take 32 us, two less without that, 47.6 with the library's
+// expf, a corrected reciprocal and a long division for each block's row.
+constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+constexpr uint32_t kGateBits = 0x42AE0000u;      // 87
+
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
-  const float c = __builtin_amdgcn_fmed3f(g, -87.0f, 104.0f);
-  const float t = c * -kLog2e;
-  const float l = __builtin_fmaf(c, -kLog2eRest, __builtin_fmaf(c, -kLog2e, -t));
+  const float t = g * -kLog2e;
+  const float l = __builtin_fmaf(g, -kLog2eRest, __builtin_fmaf(g, -kLog2e, -t));
   const float p = __builtin_amdgcn_exp2f(t), e = __builtin_fmaf(p, l * kLn2, p);
   const float r = __builtin_amdgcn_rcpf(1.0f + e);
   const float q = g * r;
   return __builtin_fmaf(q, u, __builtin_fmaf(-q, e, g - q) * r * u);
+}
+
+// The same for any g. From 87 on, 1 + e^-g is 1 in FP32, and below -87 it is e^-g, so
+// the result is g u or g e^g u. There e^g may be under FP32's range and u still bring
+// the product back into it: e^g is taken times 2^160 (t + 160 is exact), u times
+// 2^-60, and the rest follows at the end. g is taken as -180 where it is less: the
+// largest u then gives 4e-38, a code of 0 under the smallest scale, and so does
+// everything below. An infinite g leaves a NaN (-infinity times e to that), as a NaN does.
+__device__ __forceinline__ float silu_mul_any(float g, float u) {
+  if (!(fabsf(g) > 87.0f)) return silu_mul(g, u);
+  if (g > 0.0f) return g * u;
+  if (__float_as_uint(g) == 0xFF800000u) return __uint_as_float(0x7FC00000u);
+  const float c = fmaxf(g, -180.0f), t = c * kLog2e;
+  const float l = __builtin_fmaf(c, kLog2eRest, __builtin_fmaf(c, kLog2e, -t));
+  const float p = __builtin_amdgcn_exp2f(t + 160.0f), e = __builtin_fmaf(p, l * kLn2, p);
+  return __builtin_ldexpf(c * e * (u * 0x1p-60f), -100);
 }
 
 struct RowsArgs {
@@ -172,8 +188,14 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a) {
 #pragma unroll
   for (int u = 0; u < U; u++) {
     if (GATED) {
+      // The short form where it holds for every gate of the wave (four instructions to see; NaN counts as too large).
+      if (__ballot(max8(x[u]) > kGateBits) == 0) {
 #pragma unroll
-      for (int i = 0; i < 8; i++) x[u][i] = silu_mul(x[u][i], up[u][i]);
+        for (int i = 0; i < 8; i++) x[u][i] = silu_mul(x[u][i], up[u][i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[u][i] = silu_mul_any(x[u][i], up[u][i]);
+      }
     }
     const Scale k = block_scale(max16(in[u] ? max8(x[u]) : 0));
     if (in[u]) {
