@@ -494,13 +494,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(GemmArgs p) {
 // rows of 128 bytes are two loads of whole 64-byte pieces. Nothing is shared, so
 // what bounds it is memory's latency.
 template <bool GROUPED, bool F16>
-__global__ __launch_bounds__(64) void stream_kernel(GemmArgs p, uint32_t tiles_n) {
+__global__ __launch_bounds__(64) void stream_kernel(GemmArgs p, uint32_t tiles_n, uint32_t tiles) {
   constexpr int TM = 4, TN = 2;
   const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
   const int blocks = p.blocks;
 
   Tile t;
-  const uint32_t tn = blockIdx.x % tiles_n, ty = blockIdx.x / tiles_n;
+  const uint32_t at = row_workgroup(), tn = at % tiles_n, ty = at / tiles_n;
+  if (at >= tiles) return;
   if constexpr (GROUPED) {
     t.expert = ty;
     int32_t lo, hi;
@@ -656,11 +657,11 @@ template <bool GROUPED>
 static nvfp4_status launch_stream(const GemmArgs &a, int dtype, hipStream_t s) {
   const int64_t tn = (a.N + 31) / 32, ty = GROUPED ? a.experts : (a.M + 63) / 64;
   if (tn * ty > 0x7FFFFF00) return NVFP4_ERR_SHAPE;
-  const dim3 grid((unsigned)(tn * ty));
+  const dim3 grid = row_grid(tn * ty);
   if (dtype == NVFP4_F16)
-    hipLaunchKernelGGL((stream_kernel<GROUPED, true>), grid, dim3(64), 0, s, a, (uint32_t)tn);
+    hipLaunchKernelGGL((stream_kernel<GROUPED, true>), grid, dim3(64), 0, s, a, (uint32_t)tn, (uint32_t)(tn * ty));
   else
-    hipLaunchKernelGGL((stream_kernel<GROUPED, false>), grid, dim3(64), 0, s, a, (uint32_t)tn);
+    hipLaunchKernelGGL((stream_kernel<GROUPED, false>), grid, dim3(64), 0, s, a, (uint32_t)tn, (uint32_t)(tn * ty));
   NVFP4_LAUNCH_CHECK();
   return NVFP4_OK;
 }

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a) {
   const int l = threadIdx.x & 15, group = threadIdx.x >> 4;
   // The row of the workgroup's first block by one long product on the scalar unit (exact: units times blocks stay below
   // 2^64), its other blocks' from there: at most one row further, or by a short product where rows have few blocks.
-  const uint64_t unit0 = (uint64_t)blockIdx.x * (kThreads / 16 * U), row0 = a.blocks > 1 ? __umul64hi(unit0, a.inverse) : unit0;
+  const uint64_t unit0 = (uint64_t)row_workgroup() * (kThreads / 16 * U), row0 = a.blocks > 1 ? __umul64hi(unit0, a.inverse) : unit0;
   const uint32_t block0 = (uint32_t)(unit0 - row0 * (uint32_t)a.blocks);
   const uint8_t *src = static_cast<const uint8_t *>(a.x) + row0 * a.ldx * ES;
   uint8_t *dst = a.codes + row0 * a.K;
@@ -208,6 +208,7 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a) {
 struct WeightArgs {
   const void *w;
   int64_t ldw, expert_stride, N, K;
+  uint32_t count;        // of all blocks
   int32_t row_blocks, blocks;
   uint8_t *codes;
   float *scales;
@@ -220,7 +221,8 @@ template <int DT, bool FAR>
 __global__ __launch_bounds__(kThreads) void weight_kernel(WeightArgs a) {
   constexpr int ES = DT == NVFP4_F32 ? 4 : 2;
   __shared__ uint32_t tops[kThreads / 64];
-  const int64_t b = blockIdx.x;
+  const int64_t b = row_workgroup();
+  if (b >= a.count) return;
   const int64_t cb = b % a.blocks, rb = b / a.blocks % a.row_blocks, e = b / a.blocks / a.row_blocks;
   const int64_t c = cb * 128 + (threadIdx.x & 15) * 8;
   const int64_t r0 = rb * 128 + (threadIdx.x >> 4);
@@ -291,9 +293,9 @@ extern "C" nvfp4_status nvfp4_fp8_quantize(const void *x, int dtype, int64_t row
   const bool far = rows * K * (gated ? 2 : 1) * element_bytes(dtype) > kNear;
 #define ROWS(DT, FAR)                                                                                                     \
   if (gated)                                                                                                              \
-    hipLaunchKernelGGL((rows_kernel<DT, true, FAR>), dim3((unsigned)grid), dim3(kThreads), 0, (hipStream_t)stream, a);    \
+    hipLaunchKernelGGL((rows_kernel<DT, true, FAR>), row_grid(grid), dim3(kThreads), 0, (hipStream_t)stream, a);          \
   else                                                                                                                    \
-    hipLaunchKernelGGL((rows_kernel<DT, false, FAR>), dim3((unsigned)grid), dim3(kThreads), 0, (hipStream_t)stream, a)
+    hipLaunchKernelGGL((rows_kernel<DT, false, FAR>), row_grid(grid), dim3(kThreads), 0, (hipStream_t)stream, a)
   FP8_DISPATCH(dtype, far, ROWS)
 #undef ROWS
   NVFP4_LAUNCH_CHECK();
@@ -322,12 +324,12 @@ extern "C" nvfp4_status nvfp4_fp8_quantize_weight(const void *w, int dtype, int6
   a.scales = scales;
   const int64_t per = (int64_t)a.row_blocks * a.blocks;
   if (per > 0x7FFFFFFF / experts) return NVFP4_ERR_SHAPE;
-  const unsigned grid = (unsigned)(per * experts);
+  a.count = (uint32_t)(per * experts);
   nvfp4_status st = device_info(nullptr);
   if (st != NVFP4_OK) return st;
   const bool far = experts * N * K * element_bytes(dtype) > kNear;
 #define WEIGHT(DT, FAR) \
-  hipLaunchKernelGGL((weight_kernel<DT, FAR>), dim3(grid), dim3(kThreads), 0, (hipStream_t)stream, a)
+  hipLaunchKernelGGL((weight_kernel<DT, FAR>), row_grid(a.count), dim3(kThreads), 0, (hipStream_t)stream, a)
   FP8_DISPATCH(dtype, far, WEIGHT)
 #undef WEIGHT
   NVFP4_LAUNCH_CHECK();

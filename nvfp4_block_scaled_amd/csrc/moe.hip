@@ -352,8 +352,10 @@ __device__ __forceinline__ void choices(const RowArgs &a, int64_t t, int j0, int
 template <int DT, bool FAR>
 __global__ __launch_bounds__(kRowThreads) void gather_kernel(RowArgs a) {
   constexpr int N = Elem<DT>::N, ES = sizeof(typename Elem<DT>::T);
-  const int64_t t = blockIdx.x / a.parts;
-  const int c = ((int)(blockIdx.x % a.parts) * kRowThreads + (int)threadIdx.x) * N, left = a.width - c;
+  const uint32_t at = row_workgroup();
+  const int64_t t = at / a.parts;
+  if (t >= a.tokens) return;
+  const int c = ((int)(at % a.parts) * kRowThreads + (int)threadIdx.x) * N, left = a.width - c;
   u32x4_t v;
   if (left > 0) v = load_unit<DT>(static_cast<const uint8_t *>(a.x) + t * a.ldx * ES, c, left);
   for (int j0 = 0; j0 < a.top; j0 += kAhead) {
@@ -369,8 +371,10 @@ __global__ __launch_bounds__(kRowThreads) void gather_kernel(RowArgs a) {
 template <int DT, bool WEIGHTS, bool FAR>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowArgs a) {
   constexpr int N = Elem<DT>::N, ES = sizeof(typename Elem<DT>::T);
-  const int64_t t = blockIdx.x / a.parts;
-  const int c = ((int)(blockIdx.x % a.parts) * kRowThreads + (int)threadIdx.x) * N, left = a.width - c;
+  const uint32_t at = row_workgroup();
+  const int64_t t = at / a.parts;
+  if (t >= a.tokens) return;
+  const int c = ((int)(at % a.parts) * kRowThreads + (int)threadIdx.x) * N, left = a.width - c;
   float sum[N];
 #pragma unroll
   for (int i = 0; i < N; i++) sum[i] = 0.0f;
@@ -401,7 +405,8 @@ template <int DT, bool FAR>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a) {
   constexpr int N = Elem<DT>::N, ES = sizeof(typename Elem<DT>::T), WAVES = kRowThreads / 64;
   __shared__ float part[WAVES][kAhead];
-  const int64_t t = blockIdx.x;
+  const int64_t t = row_workgroup();
+  if (t >= a.tokens) return;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const uint8_t *grad = static_cast<const uint8_t *>(a.x) + t * a.ldx * ES;
   for (int j0 = 0; j0 < a.top; j0 += kAhead) {
@@ -582,7 +587,7 @@ extern "C" nvfp4_status nvfp4_moe_gather(const void *x, int dtype, int64_t ldx, 
   a.places = places;
   a.parts = (int32_t)parts;
 #define GATHER(DT, FAR) \
-  hipLaunchKernelGGL((gather_kernel<DT, FAR>), dim3((unsigned)(parts * tokens)), dim3(kRowThreads), 0, (hipStream_t)stream, a)
+  hipLaunchKernelGGL((gather_kernel<DT, FAR>), row_grid(parts * tokens), dim3(kRowThreads), 0, (hipStream_t)stream, a)
   MOE_DISPATCH(dtype, far_rows(a, es), GATHER)
 #undef GATHER
   NVFP4_LAUNCH_CHECK();
@@ -615,7 +620,7 @@ extern "C" nvfp4_status nvfp4_moe_combine(const void *y, int dtype, int64_t ldy,
   a.places = places;
   a.weights = weights;
   a.parts = (int32_t)parts;
-  const dim3 grid((unsigned)(parts * tokens));
+  const dim3 grid = row_grid(parts * tokens);
 #define COMBINE(DT, FAR) \
   hipLaunchKernelGGL((combine_kernel<DT, true, FAR>), grid, dim3(kRowThreads), 0, (hipStream_t)stream, a)
 #define SUM(DT, FAR) \
@@ -661,7 +666,7 @@ extern "C" nvfp4_status nvfp4_moe_combine_backward(const void *grad, int64_t ldg
   a.weights = weights;
   a.grad_weights = grad_weights;
 #define BACK(DT, FAR) \
-  hipLaunchKernelGGL((combine_backward_kernel<DT, FAR>), dim3((unsigned)tokens), dim3(kRowThreads), 0, (hipStream_t)stream, a)
+  hipLaunchKernelGGL((combine_backward_kernel<DT, FAR>), row_grid(tokens), dim3(kRowThreads), 0, (hipStream_t)stream, a)
   MOE_DISPATCH(dtype, far_rows(a, es), BACK)
 #undef BACK
   NVFP4_LAUNCH_CHECK();
