@@ -55,17 +55,31 @@ def _rows_out(out, name, dev, rows, cols, dtype):
 
 def _span(t):
     """Bytes from a tensor's first element to its last."""
+    if t.is_contiguous():
+        return t.nbytes
     if t.numel() == 0:
         return 0
     return (sum((n - 1) * st for n, st in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
-def _apart(out, name, *inputs):
-    """An output must not share storage with an input in the bytes that both cover."""
-    lo, hi = out.data_ptr(), out.data_ptr() + _span(out)
-    for t in inputs:
+def _outside(lo, hi, name, tensors):
+    for t in tensors:
         if t.data_ptr() < hi and lo < t.data_ptr() + _span(t):
-            raise ValueError(f"{name} overlaps an input")
+            raise ValueError(f"{name} overlaps another tensor of the call")
+
+
+def _apart(out, name, *others):
+    """What is written must not share storage with what else the call reads or writes, in the bytes that both cover."""
+    _outside(out.data_ptr(), out.data_ptr() + _span(out), name, others)
+
+
+def _work(ws, need, dev, *others):
+    """kv_cache's _bytes for a workspace, whose first `need` bytes must not share storage with the call's other tensors."""
+    given = ws is not None
+    ws, at, have = _bytes(ws, need, dev)
+    if given and need:
+        _outside(at, at + need, "ws", others)
+    return ws, at, have
 
 
 def _code_out(t, name, dev, shape, like):
@@ -78,12 +92,12 @@ def _code_out(t, name, dev, shape, like):
     return t, at
 
 
-def _scale_out(t, name, dev, shape, like):
+def _scale_out(t, name, dev, shape, like, codes):
     if t is None:
         t = like.new_empty(shape, dtype=torch.float32)
         return t, t.data_ptr()
     at = _flat(t, name, dev, torch.float32, shape)
-    _apart(t, name, like)
+    _apart(t, name, like, codes)
     return t, at
 
 
@@ -104,7 +118,7 @@ def nvfp4_fp8_quantize(x, gated=False, codes=None, scales=None):
         raise ValueError("K % 16 == 0 is required")
     x, ld = _matrix(x, "x")
     codes, codes_at = _code_out(codes, "codes", dev, (M, K), x)
-    scales, scales_at = _scale_out(scales, "scales", dev, (M, _blocks(K)), x)
+    scales, scales_at = _scale_out(scales, "scales", dev, (M, _blocks(K)), x, codes)
     _check(lib().nvfp4_fp8_quantize(x.data_ptr(), kind, M, K, ld, 1 if gated else 0, codes_at, scales_at, _stream(dev)))
     return codes, scales
 
@@ -128,7 +142,7 @@ def nvfp4_fp8_quantize_weight(w, codes=None, scales=None):
     es = es if E > 1 else 0
     lead = tuple(w.shape[:-2])
     codes, codes_at = _code_out(codes, "codes", dev, lead + (N, K), w)
-    scales, scales_at = _scale_out(scales, "scales", dev, lead + (_blocks(N), _blocks(K)), w)
+    scales, scales_at = _scale_out(scales, "scales", dev, lead + (_blocks(N), _blocks(K)), w, codes)
     _check(lib().nvfp4_fp8_quantize_weight(w.data_ptr(), kind, E, N, K, ld, es, codes_at, scales_at, _stream(dev)))
     return codes, scales
 
@@ -180,7 +194,7 @@ def nvfp4_fp8_gemm(a, a_scales, w, w_scales, out_dtype="bf16", out=None, ws=None
     if N < 1:
         raise ValueError("w has no rows")
     out, ld, kind = _out(out, out_dtype, dev, M, N, a, a_scales, w, w_scales)
-    ws, wsp, nws = _bytes(ws, lib().nvfp4_fp8_gemm_workspace_bytes(M, N, K), dev)
+    ws, wsp, nws = _work(ws, lib().nvfp4_fp8_gemm_workspace_bytes(M, N, K), dev, out, a, a_scales, w, w_scales)
     _check(lib().nvfp4_fp8_gemm(a_at, as_at, w_at, ws_at, M, N, K, out.data_ptr(), kind, ld, wsp, nws, _stream(dev)))
     return out
 

@@ -11,8 +11,8 @@ range stands for no row.
 import torch
 
 from . import _check, lib
-from .fp8 import _apart, _floats, _matrix, _rows_out
-from .kv_cache import _at, _bytes, _device, _flat, _stream
+from .fp8 import _apart, _floats, _matrix, _rows_out, _work
+from .kv_cache import _at, _device, _flat, _stream
 
 _IDS = {torch.int32: 4, torch.int64: 8}
 
@@ -34,7 +34,7 @@ def nvfp4_moe_sort(ids, experts, ws=None):
     offsets = ids.new_empty(experts + 1, dtype=torch.int32)
     tokens = ids.new_empty(T * top, dtype=torch.int32)
     places = ids.new_empty((T, top), dtype=torch.int32)
-    ws, wsp, nws = _bytes(ws, lib().nvfp4_moe_sort_workspace_bytes(T, top, experts), dev)
+    ws, wsp, nws = _work(ws, lib().nvfp4_moe_sort_workspace_bytes(T, top, experts), dev, ids)
     _check(lib().nvfp4_moe_sort(ids.data_ptr(), _IDS[ids.dtype], T, top, experts, offsets.data_ptr(), tokens.data_ptr(),
                                 places.data_ptr(), wsp, nws, _stream(dev)))
     return offsets, tokens, places
@@ -73,7 +73,7 @@ def nvfp4_moe_gather(x, places, out=None):
     dev = _device()
     at, T, top = _places(places, dev)
     x, kind, ldx, width = _input(x, "x", dev, T)
-    out, ldo = _output(out, "out", dev, T * top, width, x, x)
+    out, ldo = _output(out, "out", dev, T * top, width, x, x, places)
     _check(lib().nvfp4_moe_gather(x.data_ptr(), kind, ldx, at, T, top, width, out.data_ptr(), ldo, _stream(dev)))
     return out
 
@@ -89,7 +89,7 @@ def nvfp4_moe_combine(y, places, weights=None, out=None):
     at, T, top = _places(places, dev)
     y, kind, ldy, width = _input(y, "y", dev, T * top)
     w_at = None if weights is None else _weights(weights, dev, T, top)
-    out, ldo = _output(out, "out", dev, T, width, y, y)
+    out, ldo = _output(out, "out", dev, T, width, y, y, places, *(() if weights is None else (weights,)))
     _check(lib().nvfp4_moe_combine(y.data_ptr(), kind, ldy, at, w_at, T, top, width, out.data_ptr(), ldo, _stream(dev)))
     return out
 
@@ -112,7 +112,7 @@ def nvfp4_moe_combine_backward(grad, y, places, weights, grad_y=None):
     if columns != width:
         raise ValueError(f"grad has {columns} columns, y {width}")
     w_at = _weights(weights, dev, T, top)
-    grad_y, ldo = _output(grad_y, "grad_y", dev, T * top, width, y, y, grad)
+    grad_y, ldo = _output(grad_y, "grad_y", dev, T * top, width, y, y, grad, places, weights)
     grad_weights = y.new_empty((T, top), dtype=torch.float32)
     _check(lib().nvfp4_moe_combine_backward(grad.data_ptr(), ldg, y.data_ptr(), ldy, kind, at, w_at, T, top, width,
                                             grad_y.data_ptr(), ldo, grad_weights.data_ptr(), _stream(dev)))

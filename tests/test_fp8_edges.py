@@ -1,4 +1,4 @@
-"""FP8 in blocks where earlier tests did not look: gates far from zero."""
+"""FP8 products and the experts' operators where other tests do not look: gates far from zero, tensors of a call over one another."""
 import numpy as np
 import pytest
 import torch
@@ -60,3 +60,81 @@ def test_gates_far_from_zero_keep_nan_and_infinity(g, u):
     codes, scales = nv.nvfp4_fp8_quantize(x.cuda(), gated=True)
     assert scales.isnan().cpu().tolist() == [[False] * 3, [False, True, False], [False] * 3]
     assert int(codes.float().isnan().sum()) == 128 and bool(codes.float()[1, 128:256].isnan().all())
+
+
+class Room:
+    """Tensors at chosen bytes of one buffer."""
+
+    def __init__(self, size):
+        self.bytes = torch.zeros(size, dtype=torch.uint8, device="cuda")
+
+    def at(self, first, shape, dtype=torch.float32):
+        n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+        return self.bytes[first:first + n].view(dtype).view(shape)
+
+
+def refused(call):
+    with pytest.raises(ValueError, match="overlaps"):
+        call()
+
+
+@pytest.mark.gpu
+def test_rows_over_places_or_weights_are_refused():
+    """A workgroup would read places that another one's rows have replaced."""
+    room = Room(1 << 16)
+    places, weights = room.at(1024, (4, 2), torch.int32), room.at(2048, (4, 2))          # 32 bytes each
+    x, y = torch.ones((4, 8), device="cuda"), torch.ones((8, 8), device="cuda")
+    places.copy_(torch.arange(8, device="cuda").view(4, 2))
+    for first in (1056, 2048, 1024 - 256):                                               # behind, over the weights, before
+        nv.nvfp4_moe_gather(x, places, out=room.at(first, (8, 8)))
+    nv.nvfp4_moe_combine(y, places, out=room.at(2048, (4, 8)))
+    nv.nvfp4_moe_combine(y, places, weights, out=room.at(2080, (4, 8)))
+    nv.nvfp4_moe_combine_backward(x, y, places, weights, grad_y=room.at(2080, (8, 8)))
+    torch.cuda.synchronize()
+    assert places.flatten().tolist() == list(range(8))
+    for first in (1052, 1024, 1024 - 252):
+        refused(lambda: nv.nvfp4_moe_gather(x, places, out=room.at(first, (8, 8))))
+        refused(lambda: nv.nvfp4_moe_gather_backward(y, places, out=room.at(min(first + 128, 1052), (4, 8))))
+        refused(lambda: nv.nvfp4_moe_combine_backward(x, y, places, weights, grad_y=room.at(first, (8, 8))))
+    for first in (2076, 2048, 2048 - 124):
+        refused(lambda: nv.nvfp4_moe_combine(y, places, weights, out=room.at(first, (4, 8))))
+        refused(lambda: nv.nvfp4_moe_combine_backward(x, y, places, weights, grad_y=room.at(first, (8, 8))))
+
+
+@pytest.mark.gpu
+def test_codes_over_scales_are_refused():
+    room = Room(1 << 16)
+    x = torch.ones((4, 256), device="cuda")
+    codes = room.at(1024, (4, 256), torch.float8_e4m3fn)
+    nv.nvfp4_fp8_quantize(x, codes=codes, scales=room.at(2048, (4, 2)))
+    nv.nvfp4_fp8_quantize_weight(x, codes=codes, scales=room.at(1016, (1, 2)))
+    for first in (2044, 1024, 1024 - 28):
+        refused(lambda: nv.nvfp4_fp8_quantize(x, codes=codes, scales=room.at(first, (4, 2))))
+    refused(lambda: nv.nvfp4_fp8_quantize_weight(x, codes=codes, scales=room.at(1020, (1, 2))))
+
+
+@pytest.mark.gpu
+def test_workspaces_over_other_tensors_are_refused():
+    """As far as the call uses them; what lies behind that in a larger one is no matter."""
+    M, N, K = 4, 260, 4112
+    need = nv.lib().nvfp4_fp8_gemm_workspace_bytes(M, N, K)
+    assert need > 0
+    room = Room(need + (1 << 23))
+    sizes = [((M, K), torch.float8_e4m3fn), ((M, fp8.blocks(K)), torch.float32), ((N, K), torch.float8_e4m3fn),
+             ((fp8.blocks(N), fp8.blocks(K)), torch.float32), ((M, N), torch.bfloat16)]
+    behind, first = [], -(-need // 256) * 256
+    for shape, dtype in sizes:
+        behind.append(room.at(first, shape, dtype))
+        first += -(-int(np.prod(shape)) * 4 // 256) * 256
+    ws = room.bytes
+    nv.nvfp4_fp8_gemm(*behind[:4], out=behind[4], ws=ws)
+    for i in range(5):
+        t = list(behind)
+        t[i] = room.at((need - 1) // 256 * 256, *sizes[i])
+        refused(lambda: nv.nvfp4_fp8_gemm(*t[:4], out=t[4], ws=ws))
+    need = nv.lib().nvfp4_moe_sort_workspace_bytes(3000, 4, 64)
+    assert need > 0
+    ids = room.at(need, (3000, 4), torch.int32)
+    nv.nvfp4_moe_sort(ids, 64, ws=ws)
+    refused(lambda: nv.nvfp4_moe_sort(room.at(need - 16, (3000, 4), torch.int32), 64, ws=ws))
+    torch.cuda.synchronize()
