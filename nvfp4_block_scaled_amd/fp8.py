@@ -62,23 +62,37 @@ def _span(t):
     return (sum((n - 1) * st for n, st in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
-def _outside(lo, hi, name, tensors):
-    for t in tensors:
-        if t.data_ptr() < hi and lo < t.data_ptr() + _span(t):
-            raise ValueError(f"{name} overlaps another tensor of the call")
+def _meet(lo, hi, t):
+    """Whether the bytes lo .. hi - 1 and those from t's first element to its last have some in common."""
+    return t.data_ptr() < hi and lo < t.data_ptr() + _span(t)
+
+
+def _side_by_side(a, b):
+    """Whether two matrices of one row stride lie in different columns of it."""
+    if a.dim() != 2 or b.dim() != 2 or a.stride(1) != 1 or b.stride(1) != 1:
+        return False
+    row = a.stride(0) * a.element_size()
+    if row < 1 or row != b.stride(0) * b.element_size():
+        return False
+    first = (b.data_ptr() - a.data_ptr()) % row
+    return a.shape[1] * a.element_size() <= first <= row - b.shape[1] * b.element_size()
 
 
 def _apart(out, name, *others):
-    """What is written must not share storage with what else the call reads or writes, in the bytes that both cover."""
-    _outside(out.data_ptr(), out.data_ptr() + _span(out), name, others)
+    """What is written must not share bytes with what else the call reads or writes (of tensors that are not matrices
+    in columns of one buffer: all from the first element to the last)."""
+    lo, hi = out.data_ptr(), out.data_ptr() + _span(out)
+    for t in others:
+        if _meet(lo, hi, t) and not _side_by_side(out, t):
+            raise ValueError(f"{name} overlaps another tensor of the call")
 
 
 def _work(ws, need, dev, *others):
     """kv_cache's _bytes for a workspace, whose first `need` bytes must not share storage with the call's other tensors."""
     given = ws is not None
     ws, at, have = _bytes(ws, need, dev)
-    if given and need:
-        _outside(at, at + need, "ws", others)
+    if given and need and any(_meet(at, at + need, t) for t in others):
+        raise ValueError("ws overlaps another tensor of the call")
     return ws, at, have
 
 

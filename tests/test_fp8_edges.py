@@ -138,3 +138,37 @@ def test_workspaces_over_other_tensors_are_refused():
     nv.nvfp4_moe_sort(ids, 64, ws=ws)
     refused(lambda: nv.nvfp4_moe_sort(room.at(need - 16, (3000, 4), torch.int32), 64, ws=ws))
     torch.cuda.synchronize()
+
+
+def test_columns_of_one_buffer_lie_apart():
+    """Rows of one stride whose columns differ share no bytes, though their spans do."""
+    from nvfp4_block_scaled_amd.fp8 import _apart
+    room = torch.zeros((12, 24))
+    for out, other in ((room[:8, :8], room[:4, 8:24]), (room[:4, 8:24], room[2:10, :8]), (room[3:, 20:], room[:, 4:20]), (room[2:3, 4:8], room[:, 8:12])):
+        _apart(out, "out", other)
+        _apart(other, "out", out)
+    half = room.half()
+    _apart(half[:, :8], "out", half[:, 8:])
+    mixed = room.view(torch.uint8)[:, 40:].view(torch.bfloat16)                  # other types, the same bytes between rows
+    _apart(room[:, :10], "out", mixed)
+    for out, other in ((room[:8, :9], room[:4, 8:]), (room[:4, 7:], room[2:10, :8]), (room[:2], room[1:, 4:8]), (room[:11, :11], mixed),
+                       (room[:8, :8], room.view(24, 12)[:, 8:]), (room[:, :8], room.view(-1)[8:24]), (room.T[:8], room[:, 8:])):
+        refused(lambda: _apart(out, "out", other))
+        refused(lambda: _apart(other, "out", out))
+
+
+@pytest.mark.gpu
+def test_rows_between_columns_of_one_buffer():
+    T, top, width = 9, 3, 40
+    g = torch.Generator("cuda").manual_seed(1)
+    places = torch.randperm(T * top, generator=g, device="cuda").int().view(T, top)
+    room = torch.full((T * top, 3 * width + 2), 9.0, dtype=torch.bfloat16, device="cuda")
+    x, rows, back = room[:T, :width], room[:, width + 1:2 * width + 1], room[:T, 2 * width + 2:]
+    x.copy_(torch.randint(-4, 5, (T, width), generator=g, device="cuda"))
+    kept = x.clone()
+    nv.nvfp4_moe_gather(x, places, out=rows)
+    nv.nvfp4_moe_combine(rows, places, out=back)
+    assert torch.equal(rows[places.flatten().long()], kept.repeat_interleave(top, 0)) and torch.equal(back, top * kept) and torch.equal(x, kept)
+    _, weights = nv.nvfp4_moe_combine_backward(kept, rows, places, torch.ones((T, top), device="cuda"), grad_y=room[:, :width])
+    assert torch.equal(room[:, :width], rows) and torch.equal(weights, (kept.float() ** 2).sum(1, keepdim=True).expand(T, top))
+    assert bool((room[:, width] == 9.0).all()) and bool((room[:, 2 * width + 1] == 9.0).all())
