@@ -797,6 +797,13 @@ extern "C" size_t nvfp4_fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K
   return parts_bytes(M, N, plan_of(M, N, K).parts);
 }
 
+// For tests, which assert that their sizes reach the kernel they name (not in nvfp4.h): what a call of these sizes (0
+// experts: dense) runs on a device of so many CUs, as rows << 20 | columns << 8 | parts of a tile; 0: stream_kernel.
+extern "C" int32_t nvfp4_fp8_gemm_plan(int64_t M, int64_t N, int64_t K, int32_t experts, int32_t cus) {
+  const Plan plan = tiles_fit(K, false, 0) ? choose(M, N, K, experts, cus) : Plan();
+  return plan.shape < 0 ? 0 : kShapes[plan.shape].bm << 20 | kShapes[plan.shape].bn << 8 | plan.parts;
+}
+
 extern "C" nvfp4_status nvfp4_fp8_gemm(const uint8_t *a, const float *a_scales, const uint8_t *w, const float *w_scales,
                                        int64_t M, int64_t N, int64_t K, void *out, int dtype, int64_t ldo, void *ws,
                                        size_t ws_bytes, void *stream) {
