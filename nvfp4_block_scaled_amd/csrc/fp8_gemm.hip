@@ -140,7 +140,11 @@ __device__ __forceinline__ uint32_t count_tiles(const GemmArgs &a, uint32_t *upt
   return base;
 }
 
-// Tile t, down the rows of an expert, then across its columns.
+// Tile t, down the rows of an expert, then across its columns. The counts never
+// fall, whatever the offsets, so the expert found has the tile: upto[e - 1] <= q <
+// upto[e] bounds w by its tiles. The one exception is refused, as it could name a
+// column behind out's last: offsets that do not ascend, of 2^28 rows and more, can
+// give the experts 2^32 tiles together, where the counts start anew.
 template <int BM, int BN>
 __device__ __forceinline__ bool find_tile(const GemmArgs &a, const uint32_t *upto, uint32_t t, Tile *tile) {
   const int lane = threadIdx.x & 63;
@@ -152,7 +156,7 @@ __device__ __forceinline__ bool find_tile(const GemmArgs &a, const uint32_t *upt
   expert_rows(a, e, &lo, &hi);
   const uint32_t mine = ((uint32_t)(hi - lo) + BM - 1) / BM;
   const uint32_t w = t - (upto[e] - mine) * (uint32_t)a.tiles_n;
-  if (mine == 0 || w / mine >= (uint32_t)a.tiles_n) return false;      // only where the offsets do not ascend
+  if (mine == 0 || w / mine >= (uint32_t)a.tiles_n) return false;
   tile->expert = __builtin_amdgcn_readfirstlane(e);
   tile->m0 = __builtin_amdgcn_readfirstlane(lo + (int32_t)(w % mine) * BM);
   tile->m1 = __builtin_amdgcn_readfirstlane(hi);
