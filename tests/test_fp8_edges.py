@@ -172,3 +172,25 @@ def test_rows_between_columns_of_one_buffer():
     _, weights = nv.nvfp4_moe_combine_backward(kept, rows, places, torch.ones((T, top), device="cuda"), grad_y=room[:, :width])
     assert torch.equal(room[:, :width], rows) and torch.equal(weights, (kept.float() ** 2).sum(1, keepdim=True).expand(T, top))
     assert bool((room[:, width] == 9.0).all()) and bool((room[:, 2 * width + 1] == 9.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(300, 700, 128), (64, 3000, 5120), (1013, 1030, 4112), (2000, 2100, 1040), (5000, 4000, 528)])
+def test_how_exact_products_are(M, N, K):
+    """The matrix core's sums are off by 1.3e-5 of a result in the mean square on gaussian rows, whatever K (blocks' errors and
+    results grow alike); twice that is allowed here. It is a sixteenth of FP16's rounding and still seen: an output is e + d
+    rounded, d what the sums are off, so the mean of (out - e)^2 is that of d^2 and of the rounding's square, and the latter is
+    that of (round(e) - e)^2 but for chance. Only the outputs that d carries over a tie differ there, 2 |d| / step or some
+    3 % of them (under 10 %), each by some 1e-8 of the result's square: over 210000 outputs a hundredth of what is allowed."""
+    r = np.random.default_rng(K)
+    x = torch.from_numpy(r.standard_normal((M, K)).astype(np.float32)).cuda()
+    y = torch.from_numpy(r.standard_normal((N, K)).astype(np.float32) * np.float32(K ** -0.5)).cuda()
+    a, sa = nv.nvfp4_fp8_quantize(x)
+    w, sw = nv.nvfp4_fp8_quantize_weight(y)
+    number = torch.from_numpy(fp8.values(np.arange(256).astype(np.uint8))).cuda()
+    wide = lambda s: s.double().repeat_interleave(128, 1)[:, :K]      # noqa: E731
+    want = (number[a.view(torch.uint8).int()] * wide(sa)) @ (number[w.view(torch.uint8).int()] * wide(sw).repeat_interleave(128, 0)[:N]).T
+    got = nv.nvfp4_fp8_gemm(a, sa, w, sw, out_dtype="f16").double()
+    off = float(((got - want) ** 2 - (want.half().double() - want) ** 2).mean() / (want ** 2).mean())
+    assert off <= (2 * 1.3e-5) ** 2, off
+    assert float((got != want.half().double()).double().mean()) < 0.1
