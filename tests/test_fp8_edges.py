@@ -194,3 +194,69 @@ def test_how_exact_products_are(M, N, K):
     off = float(((got - want) ** 2 - (want.half().double() - want) ** 2).mean() / (want ** 2).mean())
     assert off <= (2 * 1.3e-5) ** 2, off
     assert float((got != want.half().double()).double().mean()) < 0.1
+
+
+def test_transposed_codes_and_scales_are_those_of_the_transposed_weight():
+    """Blocks of 128 x 128 are the same ones either way, whole or cut."""
+    w = np.random.default_rng(3).standard_normal((272, 400)).astype(np.float32)
+    (c, s), (ct, st) = fp8.quantize(w, 128), fp8.quantize(np.ascontiguousarray(w.T), 128)
+    np.testing.assert_array_equal(c.T, ct)
+    np.testing.assert_array_equal(s.T, st)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,top,experts,N,K", [(5, 2, 3, 48, 272), (300, 3, 6, 272, 400), (1500, 2, 4, 528, 144)])
+def test_gradient_of_the_input_of_products_by_expert(T, top, experts, N, K):
+    """Of sum(c combine(products(x))) to x, through the public calls alone: combine's gradient, quantized, by the transposed
+    weights, summed over each token's rows. In FP8 the rows' gradients are within half a step of E4M3 (2^-4 of the value, at
+    least 2^-10 of a scale), their products as exact as any, each rounded to BF16, and so is the sum."""
+    r = np.random.default_rng(T)
+    w, sw = nv.nvfp4_fp8_quantize_weight(torch.from_numpy(r.standard_normal((experts, N, K)).astype(np.float32) * np.float32(K ** -0.5)).cuda())
+    ids = torch.from_numpy(np.argsort(r.random((T, experts)), 1)[:, :top].astype(np.int32)).cuda()
+    ids[::4, 0] = -1
+    offsets, tokens, places = nv.nvfp4_moe_sort(ids, experts)
+    weights = torch.from_numpy(r.random((T, top)).astype(np.float32)).cuda()
+    x, c = (torch.from_numpy(r.standard_normal(n).astype(np.float32)).to(torch.bfloat16).cuda() for n in ((T, K), (T, N)))
+    a, sa = nv.nvfp4_fp8_quantize(x)
+    y = torch.zeros((T * top, N), dtype=torch.bfloat16, device="cuda")
+    nv.nvfp4_fp8_gemm_grouped(a, sa, w, sw, offsets, rows=tokens, out=y)
+
+    wt, swt = w.view(torch.uint8).transpose(1, 2).contiguous(), sw.transpose(1, 2).contiguous()
+    grad_y, _ = nv.nvfp4_moe_combine_backward(c, y, places, weights, grad_y=torch.zeros_like(y))
+    g, sg = nv.nvfp4_fp8_quantize(grad_y)
+    rows = torch.zeros((T * top, K), dtype=torch.bfloat16, device="cuda")
+    nv.nvfp4_fp8_gemm_grouped(g, sg, wt, swt, offsets, out=rows)
+    got = nv.nvfp4_moe_gather_backward(rows, places).double().cpu().numpy()
+
+    held = np.stack([fp8.values(c) * fp8.spread(s.astype(np.float64), 128, c.shape) for c, s in zip(w.view(torch.uint8).cpu().numpy(), sw.cpu().numpy())])
+    ids, c, weights, sg, places = (t.double().cpu().numpy() for t in (ids, c, weights, sg, places))
+    want, tol, total = np.zeros((T, K)), np.zeros((T, K)), np.zeros((T, K))
+    wide = fp8.spread(sg, 1, (T * top, N))
+    for t in range(T):
+        for j in range(top):
+            e = int(ids[t, j])
+            if e < 0:
+                continue
+            grad = weights[t, j] * c[t]
+            part, size = grad @ held[e], np.abs(grad) @ np.abs(held[e])
+            off = np.maximum(2.0 ** -4 * np.abs(grad), 2.0 ** -10 * wide[int(places[t, j])]) + 2.0 ** -8 * np.abs(grad)      # and BF16 before
+            inner = off @ np.abs(held[e]) * 1.01 + (7 * 2.0 ** -13 + (N / 8 + 3 * fp8.blocks(N)) * 2.0 ** -24) * size * 1.1
+            want[t] += part
+            tol[t] += inner + 2.0 ** -8 * (np.abs(part) + inner)
+            total[t] += np.abs(part) + inner
+    assert (np.abs(got - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol) + 2.0 ** -20 * total + 1e-30).all()
+    # in the mean square FP8 alone: an error of up to 2^-4 of a value either way is 2^-4 / sqrt(3), 0.036, at most
+    assert np.sqrt(((got - want) ** 2).mean() / (want ** 2).mean()) < 0.05
+
+    def loss(v):      # in float64, from x's values
+        out = np.zeros((T, N))
+        for t in range(T):
+            for j in range(top):
+                if ids[t, j] >= 0:
+                    out[t] += weights[t, j] * (held[int(ids[t, j])] @ v[t])
+        return (out * c).sum()
+    v, h = x.double().cpu().numpy(), 1e-3
+    for t, k in ((0, 0), (T - 1, K - 1), (T // 2, 130)):
+        step = np.zeros_like(v)
+        step[t, k] = h                                                            # linear in x: exact but for rounding
+        assert abs((loss(v + step) - loss(v - step)) / (2 * h) - got[t, k]) <= tol[t, k] + 2.0 ** -7 * total[t, k] + 1e-6
