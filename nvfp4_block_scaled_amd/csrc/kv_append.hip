@@ -452,9 +452,6 @@ nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache *cache, nvfp4_rows k, nvfp4_ro
   if (rope && rope->rot_dim > 0 &&
       (!aligned(rope->cos, 4) || !aligned(rope->sin, 4) || !aligned(rope->positions, 4)))
     return NVFP4_ERR_ALIGN;
-  DeviceInfo d;
-  st = device_info(&d);
-  if (st != NVFP4_OK) return st;
 
   A.k = (const uint16_t *)k.base, A.k_t = k.token_stride, A.k_h = k.head_stride;
   A.v = (const uint16_t *)v.base, A.v_t = v.token_stride, A.v_h = v.head_stride;
@@ -472,7 +469,10 @@ nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache *cache, nvfp4_rows k, nvfp4_ro
   A.chunks = A.turn_chunks + (D - A.rot + 15) / 16;
   const int per_wg = kAppendThreads / A.chunks;
   const int64_t wgs = (tokens + per_wg - 1) / per_wg;
-  if (wgs > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
+  if (wgs > kMostWorkgroups) return NVFP4_ERR_SHAPE;
+  DeviceInfo d;
+  st = device_info(&d);
+  if (st != NVFP4_OK) return st;
   // Sixteen heads to a group share one read of the table (8192 tokens of 48 heads, replayed in a graph:
   // 33.3 us, 35.3 with eight); with few tokens, fewer heads to a group fill the CUs instead (64 tokens:
   // 4.3 us with one, 5.8 with two, 8.8 with four to sixteen).
@@ -507,7 +507,7 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int64_t *slots, in
   if (!slots || !k.base || !v.base) return NVFP4_ERR_NULL;
   if (!kv_rows_aligned(k) || !kv_rows_aligned(v) || !aligned(slots, 8)) return NVFP4_ERR_ALIGN;
   const int64_t per_token = (int64_t)A.kv.heads * (A.kv.D / 16);
-  if (tokens > ((int64_t)0x7FFFFFFF * 256) / per_token) return NVFP4_ERR_SHAPE;
+  if (tokens > kMostWorkgroups * 256 / per_token) return NVFP4_ERR_SHAPE;
   DeviceInfo d;
   st = device_info(&d);
   if (st != NVFP4_OK) return st;

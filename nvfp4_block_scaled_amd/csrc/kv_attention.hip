@@ -1387,7 +1387,7 @@ static bool plan_launch(const KvView &kv, int64_t total_q, int32_t q_heads, int6
   L->few = L->joins * kv.heads <= 32;
   const int in_join = L->nt < 8 ? 1 : (L->few ? 256 : 1024) / DP;
   L->rows = (int)(((most_rows < RT ? most_rows : RT) + in_join - 1) / in_join * in_join);
-  return L->units * kv.heads < 0x7FFFFFFF && L->joins * RT * kv.heads <= 0x7FFFFFFF && steps * tiles <= 0x3FFFFFFF;
+  return L->units * kv.heads < kMostWorkgroups && L->joins * RT * kv.heads <= kMostWorkgroups && steps * tiles <= 0x3FFFFFFF;
 }
 
 // Partial sums, (m, l), and the list of what is joined.

@@ -30,6 +30,10 @@ struct KvView {
   __host__ __device__ __forceinline__ uint32_t head_bytes() const { return ((uint32_t)D << log_p) / 8 * 9; }
 };
 
+// The most workgroups of 256 threads in a launch along one dimension: the runtime
+// counts threads in 32 bits and drops the rest without an error.
+constexpr int64_t kMostWorkgroups = 0xFFFFFF;
+
 // CUs of the current device; 256 where there is none (config.hip).
 int device_cus_or_default();
 

@@ -208,11 +208,12 @@ __global__ __launch_bounds__(kScanThreads) void fork_plan_kernel(const ForkArgs 
 // Copies pages (the first blocks of the grid), writes the children's rows and raises the counts of
 // shared pages (the last `children` blocks).
 __global__ __launch_bounds__(kCopyThreads) void fork_copy_kernel(const ForkArgs A, int copy_blocks) {
-  if ((int)blockIdx.x < copy_blocks) {
-    copy_pairs(A.pool, A.src, A.dst, A.children, blockIdx.x, copy_blocks);
+  const int at = row_workgroup(), c = at - copy_blocks;
+  if (c < 0) {
+    copy_pairs(A.pool, A.src, A.dst, A.children, at, copy_blocks);
     return;
   }
-  const int c = blockIdx.x - copy_blocks;
+  if (c >= A.children) return;
   const int dst = A.dst[c];
   const bool ok = dst != -2;
   const int p = ok ? A.parents[c] : 0;
@@ -242,7 +243,8 @@ struct ResizeArgs {
 
 // A workgroup per sequence: gives back what it drops and writes its row: kept entries, -1 elsewhere.
 __global__ __launch_bounds__(256) void resize_rows_kernel(const ResizeArgs A) {
-  const int b = blockIdx.x;
+  const int b = row_workgroup();
+  if (b >= A.batch) return;
   const int was = (clamp_len(A.lens[b], A.width, A.log_p) + (1 << A.log_p) - 1) >> A.log_p;
   const int now = (clamp_len(A.new_lens[b], A.width, A.log_p) + (1 << A.log_p) - 1) >> A.log_p;
   const bool in_place = A.table == A.table_out;
@@ -543,7 +545,7 @@ nvfp4_status nvfp4_kv_fork(const nvfp4_kv_pool *pool, int32_t page_size, const i
   NVFP4_LAUNCH_CHECK();
   if (children == 0) return NVFP4_OK;
   const int copies = copy_grid(A.pool, children, d.num_cus);
-  hipLaunchKernelGGL(fork_copy_kernel, dim3((unsigned)(copies + children)), dim3(kCopyThreads), 0, s, A, copies);
+  hipLaunchKernelGGL(fork_copy_kernel, row_grid(copies + children), dim3(kCopyThreads), 0, s, A, copies);
   NVFP4_LAUNCH_CHECK();
   return NVFP4_OK;
 }
@@ -573,7 +575,7 @@ nvfp4_status nvfp4_kv_resize(int64_t num_pages, int32_t page_size, const int32_t
   A.table_out = table_out, A.refs = refs_out, A.short_dev = short_dev;
   A.starts = (int32_t *)ws, A.taken = A.starts + batch;    // (batch + num_pages <= 3 max(batch, num_pages))
   if ((st = copy_counts(refs, refs_out, num_pages, s)) != NVFP4_OK) return st;
-  hipLaunchKernelGGL(resize_rows_kernel, dim3((unsigned)batch), dim3(256), 0, s, A);
+  hipLaunchKernelGGL(resize_rows_kernel, row_grid(batch), dim3(256), 0, s, A);
   NVFP4_LAUNCH_CHECK();
   hipLaunchKernelGGL(resize_plan_kernel, dim3(1), dim3(kScanThreads), 0, s, A);
   NVFP4_LAUNCH_CHECK();
