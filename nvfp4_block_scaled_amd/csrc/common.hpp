@@ -98,20 +98,7 @@ __device__ __forceinline__ float col_alpha(float al, const float *alpha_col, int
   return alpha_col ? al * alpha_col[n] : al;
 }
 
-// The number of a workgroup in a launch over row_grid().
-constexpr int kRowShift = 22;
-__device__ __forceinline__ uint32_t row_workgroup() { return (blockIdx.y << kRowShift) + blockIdx.x; }
-
 // ---------------------------------------------------------------- host side
-
-// A launch of n (up to 2^31 - 1) workgroups of at most 512 threads. Along one
-// dimension the runtime counts threads in 32 bits and drops the rest without an
-// error, so past 2^22 workgroups they go on along the next; those from n on are
-// surplus and leave.
-inline dim3 row_grid(int64_t n) {
-  const int64_t row = int64_t(1) << kRowShift;
-  return n <= row ? dim3((unsigned)n) : dim3((unsigned)row, (unsigned)((n + row - 1) / row));
-}
 
 struct DeviceInfo {
   int device = -1;

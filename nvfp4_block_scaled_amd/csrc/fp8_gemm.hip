@@ -25,6 +25,7 @@
 #include <algorithm>
 
 #include "common.hpp"
+#include "launch.hpp"
 
 namespace nvfp4 {
 

@@ -16,6 +16,7 @@
 // only where it underflows, far below E4M3's smallest code.
 #include "common.hpp"
 #include "kv_common.hpp"
+#include "launch.hpp"
 
 namespace nvfp4 {
 namespace fp8 {

@@ -12,6 +12,7 @@
 // latency of a few dependent passes over the counts: 5 to 7 us before a copy, 11.3
 // for a resize of 256 sequences in a pool of 65536 pages (three launches).
 #include "kv_common.hpp"
+#include "launch.hpp"
 
 namespace nvfp4 {
 

@@ -13,6 +13,7 @@
 // same bits on every call), and only rows that a place names are written.
 #include "common.hpp"
 #include "kv_common.hpp"
+#include "launch.hpp"
 
 namespace nvfp4 {
 namespace moe {
