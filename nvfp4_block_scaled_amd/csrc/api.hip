@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "common.hpp"
+#include "launch.hpp"
 
 namespace nvfp4 {
 
@@ -57,7 +58,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(const uint8_t *__restrict_
                                                       int32_t *bad_count) {
   const int64_t nblk = K / 16;
   const int64_t total = N * nblk;
-  const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t idx = (int64_t)row_workgroup() * 256 + threadIdx.x;
   if (idx >= total) return;
   const int64_t n = idx / nblk;
   const int64_t b = idx - n * nblk;
@@ -162,7 +163,7 @@ nvfp4_status nvfp4_prepare_weight(const uint8_t *w_codes, const uint8_t *w_scale
   const int64_t total = N * (K / 16);
   const int64_t grid = (total + 255) / 256;
   if (grid > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
-  hipLaunchKernelGGL(prepare_kernel, dim3((unsigned)grid), dim3(256), 0, s, w_codes, w_scales, scale_kind, N, K,
+  hipLaunchKernelGGL(prepare_kernel, row_grid(grid), dim3(256), 0, s, w_codes, w_scales, scale_kind, N, K,
                      w_prep, bad_count_dev);
   NVFP4_LAUNCH_CHECK();
   return NVFP4_OK;
