@@ -1498,6 +1498,10 @@ size_t w4a16_config_workspace_bytes(int64_t M, int64_t N, int64_t K, const nvfp4
 
 using namespace nvfp4;
 
+// Whether a launch along one dimension runs whole: the runtime counts its threads
+// in 32 bits and drops the rest without an error.
+static bool launch_fits(int64_t grid, int waves) { return grid <= 0xFFFFFFFFll / (waves * 64); }
+
 extern "C" nvfp4_status nvfp4_gemm_w4a16(const uint16_t *x, int64_t ldx, const uint8_t *w_prep, int64_t M, int64_t N,
                                          int64_t K, float alpha, const float *alpha_dev, const float *alpha_col,
                                          uint16_t *y, int64_t ldy, const nvfp4_config *config, void *ws,
@@ -1521,7 +1525,7 @@ extern "C" nvfp4_status nvfp4_gemm_w4a16(const uint16_t *x, int64_t ldx, const u
   if (need > 0 && !aligned(ws, 16)) return NVFP4_ERR_ALIGN;
   hipStream_t s = (hipStream_t)stream;
   if (plan.kind == 0) {
-    if (plan.grid_x > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
+    if (!launch_fits(plan.grid_x, w4a16::kDecodeShapes[plan.dec].W)) return NVFP4_ERR_SHAPE;
     const size_t lds = (size_t)(M * K * 2);
     const int key = plan.dec * 8 + (int)M;
 #define NVFP4_DECODE_CASE(D, MM)                                                                               \
@@ -1583,9 +1587,10 @@ extern "C" nvfp4_status nvfp4_gemm_w4a16(const uint16_t *x, int64_t ldx, const u
     }
 #undef NVFP4_BIG
   } else if (plan.kind == 3) {
-    if (plan.grid_x > 0x7FFFFFFF || M * ldx * 2 > 0xFFFFFFFFll) return NVFP4_ERR_SHAPE;
+    if (M * ldx * 2 > 0xFFFFFFFFll) return NVFP4_ERR_SHAPE;
     const int MT = M <= 32 ? 1 : 2;
     const w4a16::SkinnyShape sh = w4a16::skinny_shape(M, N, K, cfg.num_cus);
+    if (!launch_fits(plan.grid_x / sh.NG, sh.W)) return NVFP4_ERR_SHAPE;
     const bool xf_path = sh.RP == 0 && M > w4a16::kSkinnyDirectMaxM;
     if (xf_path && (int64_t)MT * 64 * K > 0x7FFFFFFFll) return NVFP4_ERR_SHAPE;   // 32-bit fragment offsets
     uint8_t *xf = static_cast<uint8_t *>(ws);
