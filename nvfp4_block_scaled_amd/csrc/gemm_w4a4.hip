@@ -45,6 +45,7 @@
 // k = 32h + 8s + i. A and W use the same map, so the sum over steps covers the
 // chunk exactly once, and each dword lies inside one 16-block (block 2h + s/2).
 #include "common.hpp"
+#include "launch.hpp"
 
 namespace nvfp4 {
 namespace w4a4 {
@@ -67,7 +68,7 @@ __global__ __launch_bounds__(256) void tile_a_kernel(const uint8_t *__restrict__
                                                      uint8_t *__restrict__ at) {
   const int64_t kt = K / 64;
   const int64_t Mp = padded_rows(M);
-  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t u = (int64_t)row_workgroup() * 256 + threadIdx.x;
   const int64_t tile = u >> 6;
   if (tile >= Mp / 32 * kt) return;
   const int unit = (int)(u & 63), h = unit >> 5, r = unit & 31;
@@ -822,7 +823,7 @@ nvfp4_status launch_gemm(const uint8_t *a_tiled, const uint8_t *w_prep, int64_t 
 void launch_tile_a(const uint8_t *a_codes, const uint8_t *a_scales, int64_t M, int64_t K, uint8_t *at,
                    hipStream_t s) {
   const int64_t units = w4a4::padded_rows(M) / 32 * (K / 64) * 64;
-  hipLaunchKernelGGL(w4a4::tile_a_kernel, dim3((unsigned)((units + 255) / 256)), dim3(256), 0, s, a_codes, a_scales,
+  hipLaunchKernelGGL(w4a4::tile_a_kernel, row_grid((units + 255) / 256), dim3(256), 0, s, a_codes, a_scales,
                      M, K, at);
 }
 

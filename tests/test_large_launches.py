@@ -1,5 +1,5 @@
 """Calls with 2^32 threads and more, which the runtime drops the rest of along one dimension: a weight of 2^36 values is prepared
-whole, and W4A16 products of so many columns that their launch does not run whole are refused."""
+whole, an activation of 2^37 is tiled whole, and W4A16 products of so many columns that their launch does not run whole are refused."""
 import pytest
 import torch
 
@@ -20,6 +20,20 @@ def test_prepare_weight_of_many_blocks():
         want, _ = nv.nvfp4_prepare_weight(codes[at:at + n], scales[at:at + n])
         assert torch.equal(whole[at * (K // 2):(at + n) * (K // 2)], want[:n * (K // 2)])
         first = N * (K // 2) + at * (K // 16)
+        assert torch.equal(whole[first:first + n * (K // 16)], want[n * (K // 2):])
+
+
+def test_tile_activation_of_many_units():
+    """As the weight above; tiles of codes, then those of scales."""
+    M, K, part = (1 << 20) + 32, 1 << 17, 1 << 16
+    codes = torch.empty((M, K // 2), dtype=torch.uint8, device="cuda").random_()
+    scales = torch.empty((M, K // 16), dtype=torch.uint8, device="cuda").random_()
+    whole = nv.nvfp4_tile_activation(codes, scales)
+    for at in range(0, M, part):
+        n = min(part, M - at)
+        want = nv.nvfp4_tile_activation(codes[at:at + n], scales[at:at + n])
+        assert torch.equal(whole[at * (K // 2):(at + n) * (K // 2)], want[:n * (K // 2)])
+        first = M * (K // 2) + at * (K // 16)
         assert torch.equal(whole[first:first + n * (K // 16)], want[n * (K // 2):])
 
 
