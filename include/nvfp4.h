@@ -435,13 +435,13 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache *cache, const int64_t *slots, in
  *          not computed. The kernels are chosen by it.
  *  mask    device uint8 [total_q][max_q], rows mask_stride apart, or NULL.
  *  lse     device FP32 [total_q][q_heads], or NULL.
- * A workgroup has one KV head and up to 16 query rows (of many rows a sequence,
- * 128); calls of 2^24 workgroups, as of 2^20 sequences with 16 KV heads, are
- * refused (NVFP4_ERR_SHAPE).
  *  ws      nvfp4_kv_attention_workspace_bytes(...) bytes, 16-byte aligned, no
  *          initialisation needed; one per stream that runs concurrently. Its
  *          size depends on the current device's CUs: ask on the device of the
  *          call.
+ * A workgroup has one KV head and up to 16 query rows of a sequence (128 where
+ * there are many); calls of 2^24 workgroups, as of 2^20 sequences with 16 KV
+ * heads, are refused (NVFP4_ERR_SHAPE).
  * Long sequences are split over the CUs and joined in a fixed order: results
  * are bit-identical from call to call. How far they are split, the workspace
  * and the second launch follow max_pages, not the lengths, which the host does
